@@ -336,6 +336,133 @@ NVFP4_API nvfp4_status nvfp4_attention_decode(const void *q, int64_t ldq, int32_
                                               void *workspace, size_t workspace_bytes,
                                               void *stream);
 
+/* ---- paged KV cache ---------------------------------------------------- */
+/* A serving loop's cache ("FP4 KV-cache quantization": every generated token
+ * re-reads the whole cache, so it is kept in NVFP4 and restored on the fly).
+ * A pool is a pair of nvfp4_tensors K, V of equal shape with LINEAR scales:
+ * rows = pages * page_size token rows, cols = heads * head_dim, each under a
+ * tensor scale that the caller sets once (the cache grows token by token, so
+ * g comes from calibration; values past 448 * 6 / g saturate).  A sequence's
+ * pages are any rows of the pool, listed by its block table; the identity
+ * table makes a pool the contiguous cache of nvfp4_attention_decode.
+ * Rows are named by int32 slots (page * page_size + offset); slot -1 names no
+ * row (padding of a captured batch).  A slot, position or page outside of its
+ * range is not followed: the row is skipped and NVFP4_ERR_INVALID_ARG is
+ * recorded in the workspace's status word.  Only the 256-byte status block of
+ * a workspace is used. */
+
+/* Rotary frequencies for nvfp4_rope_table, on the host: inv_freq[i], i <
+ * rotary_dim / 2, from f_i = base^(-2i / rotary_dim) (base > 1).
+ *   PLAIN   f_i
+ *   LINEAR  f_i / factor (positions interpolated)
+ *   NTK     base * factor^(rotary_dim / (rotary_dim - 2)) in place of base
+ *   BANDS   a f_i + (1 - a) f_i / factor, a = clamp((L f_i / 2pi - low) /
+ *           (high - low), 0, 1): by the turns a pair makes over the original
+ *           L = original_positions positions
+ *   RAMP    the same mix with a = 1 - clamp((i - i0) / (i1 - i0), 0, 1), i0 =
+ *           max(floor(d(high)), 0), i1 = min(ceil(d(low)), rotary_dim - 1)
+ *           (i0 + 0.001 where i1 <= i0), d(b) = rotary_dim ln(L / (2pi b)) /
+ *           (2 ln base): linear in the pair's index between the pairs that
+ *           make `high` and `low` turns
+ * Arguments that a kind does not name are ignored. */
+typedef enum {
+    NVFP4_ROPE_PLAIN = 0,
+    NVFP4_ROPE_LINEAR = 1,
+    NVFP4_ROPE_NTK = 2,
+    NVFP4_ROPE_BANDS = 3,
+    NVFP4_ROPE_RAMP = 4
+} nvfp4_rope_scaling;
+NVFP4_API nvfp4_status nvfp4_rope_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
+                                           double factor, double original_positions, double low,
+                                           double high, double *inv_freq);
+
+/* d_table[r][i] = (magnitude cos a, magnitude sin a), a = (first_position +
+ * r) * d_inv_freq[i]: [rows x rotary_dim / 2] pairs of float, 16-byte
+ * aligned, the angles formed in FP64 and each value rounded once.  Made once
+ * and used by every layer. */
+NVFP4_API nvfp4_status nvfp4_rope_table(const double *d_inv_freq, int32_t rotary_dim,
+                                        int64_t first_position, int64_t rows, double magnitude,
+                                        float *d_table, void *stream);
+
+/* Rotary positions: of each head's head_dim values the first rotary_dim are
+ * rotated in pairs -- (i, i + rotary_dim / 2), or (2i, 2i + 1) if interleaved
+ * -- by row d_positions[t] of the table:
+ *   y1 = RN(RN(x1 c) - RN(x2 s)), y2 = RN(RN(x2 c) + RN(x1 s)), then BF16;
+ * the others are copied.  inverse = 1 takes -s: the transposed map, that is
+ * the gradient of x from the gradient of y.
+ * x, y: BF16 [tokens][heads][head_dim], innermost contiguous, strides in
+ *   elements (x may repeat rows by a stride of 0; y's rows may not overlap).
+ *   y == x with equal strides works in place; they may not overlap in part.
+ *   2-byte aligned; 16-byte aligned pieces (strides % 8 == 0, rotary_dim % 16
+ *   == 0, or % 8 if interleaved) take the vectorised path.
+ * d_positions: int32[tokens]; position -1 leaves the token's y as it was.
+ * rotary_dim: even, 2 .. head_dim.  tokens * heads * head_dim < 2^31 pieces. */
+NVFP4_API nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride,
+                                  int64_t tokens, int32_t heads, int32_t head_dim,
+                                  const int32_t *d_positions, const float *d_table,
+                                  int64_t table_rows, int32_t rotary_dim, int32_t interleaved,
+                                  int32_t inverse, void *y, int64_t y_token_stride,
+                                  int64_t y_head_stride, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
+/* Write tokens into the cache: pool row d_slots[t] of K gets the NVFP4 of
+ * k[t], of V that of v[t], quantized as nvfp4_quantize does with the tensor
+ * scale already in K->global / V->global (same bytes).  With a table the keys
+ * are first rotated as nvfp4_rope does (rounded to BF16); a token whose
+ * position has no table row (-1, or out of range) is then not written.
+ * d_table == NULL: no rotation, the rotary arguments are ignored.
+ * k, v: BF16 [tokens][heads][head_dim], strides in elements, multiples of 8;
+ *   16-byte aligned.  head_dim % 16 == 0, heads * head_dim == K->cols.
+ * Two tokens of one call may not name the same slot (the row would hold parts
+ * of both).  Non-finite values are recorded as NVFP4_ERR_NONFINITE; the
+ * 16-value block that holds them is then unspecified. */
+NVFP4_API nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                                      const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                                      int64_t tokens, int32_t heads, int32_t head_dim,
+                                      const int32_t *d_slots, const nvfp4_tensor *K,
+                                      const nvfp4_tensor *V, const int32_t *d_positions,
+                                      const float *d_table, int64_t table_rows, int32_t rotary_dim,
+                                      int32_t interleaved, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* Read rows back: k[r], v[r] = BF16 of pool row d_slots[r] of K and V, as
+ * nvfp4_dequantize restores them; slot -1 (or out of range) gives zeros.
+ * k, v: BF16 [rows x cols], pitches ldk, ldv elements (multiples of 8),
+ * 16-byte aligned.  For the dense attention of a prompt chunk over what is
+ * cached already. */
+NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V,
+                                     const int32_t *d_slots, int64_t rows, void *k, int64_t ldk,
+                                     void *v, int64_t ldv, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/* Decode attention of a batch over the paged cache: one query token a
+ * sequence, grouped-query heads (query head h reads KV head h / (heads_q /
+ * heads_kv)), over the first d_seq_lens[b] tokens of sequence b; token t is
+ * pool row d_block_table[b * table_stride + t / page_size] * page_size + t %
+ * page_size:
+ *   s_t = scale * q_h . k_t,  o_h = sum_t exp(s_t) v_t / sum_t exp(s_t),
+ *   d_lse[b * heads_q + h] = log sum_t exp(s_t)   (d_lse may be NULL)
+ * with k, v the exact restored values.  A sequence of length 0 gives o = 0
+ * and lse = -inf.  A length past table_pages * page_size (or below 0) is cut
+ * to it (to 0) and recorded as NVFP4_ERR_INVALID_ARG; tokens on a page
+ * outside of the pool take no part and are recorded alike.
+ * q, o  : BF16 [sequences][heads_q][head_dim], strides in elements, multiples
+ *         of 8; 16-byte aligned.  head_dim = K->cols / heads_kv: 64, 128, 256.
+ * page_size: any; K->rows a multiple of it and below 2^31.
+ * scratch: nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, head_dim)
+ *   bytes, 16-byte aligned, of any content; calls that may run at the same
+ *   time need scratch of their own (they may share the workspace, of which
+ *   only the status block is used).
+ * Results depend on the sequences' lengths and the batch, not on timing. */
+NVFP4_API size_t nvfp4_attention_paged_scratch_bytes(int32_t heads_q, int32_t heads_kv,
+                                                     int32_t head_dim);
+NVFP4_API nvfp4_status nvfp4_attention_decode_paged(
+    const void *q, int64_t q_seq_stride, int64_t q_head_stride, int32_t sequences, int32_t heads_q,
+    const nvfp4_tensor *K, const nvfp4_tensor *V, int32_t heads_kv, const int32_t *d_block_table,
+    int64_t table_stride, int32_t table_pages, const int32_t *d_seq_lens, int32_t page_size,
+    float scale, void *o, int64_t o_seq_stride, int64_t o_head_stride, float *d_lse,
+    void *workspace, size_t workspace_bytes, void *scratch, size_t scratch_bytes, void *stream);
+
 /* ---- MXFP4 ------------------------------------------------------------ */
 /* MXFP4, the format the pages compare NVFP4 with ("NVIDIA shrank GLM-5.2 to
  * 4 bits", section 3: blocks of 32 with a power-of-two E8M0 scale; "NVFP4:

@@ -9,6 +9,7 @@ tensors instead of raw pointers.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -40,8 +41,12 @@ EXPORTED = (
     "nvfp4_quantize_noalloc", "nvfp4_quantize_rht", "nvfp4_quantize_t", "nvfp4_quantize_2d",
     "nvfp4_quantize_sr", "nvfp4_mx_scales_bytes", "nvfp4_quantize_mx", "nvfp4_dequantize_mx",
     "nvfp4_gemm_mx", "nvfp4_moe_combine", "nvfp4_dequantize_fp8", "nvfp4_quantize_swiglu",
-    "nvfp4_attention_decode", "nvfp4_gather_rows",
+    "nvfp4_attention_decode", "nvfp4_gather_rows", "nvfp4_rope_inv_freq", "nvfp4_rope_table",
+    "nvfp4_rope", "nvfp4_kv_write", "nvfp4_kv_read", "nvfp4_attention_paged_scratch_bytes",
+    "nvfp4_attention_decode_paged",
 )
+
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "ramp": 4}
 
 
 class NVFP4Error(RuntimeError):
@@ -103,6 +108,18 @@ def lib() -> C.CDLL:
             "nvfp4_quantize_swiglu": (C.c_int, [vp, i64, T, vp, sz, vp]),
             "nvfp4_attention_decode": (C.c_int, [vp, i64, i32, T, T, i32, C.c_float, vp, i64, vp, sz,
                                                  vp]),
+            "nvfp4_rope_inv_freq": (C.c_int, [i32, C.c_double, i32, C.c_double, C.c_double, C.c_double,
+                                              C.c_double, vp]),
+            "nvfp4_rope_table": (C.c_int, [vp, i32, i64, i64, C.c_double, vp, vp]),
+            "nvfp4_rope": (C.c_int, [vp, i64, i64, i64, i32, i32, vp, vp, i64, i32, i32, i32, vp, i64,
+                                     i64, vp, sz, vp]),
+            "nvfp4_kv_write": (C.c_int, [vp, i64, i64, vp, i64, i64, i64, i32, i32, vp, T, T, vp, vp,
+                                         i64, i32, i32, vp, sz, vp]),
+            "nvfp4_kv_read": (C.c_int, [T, T, vp, i64, vp, i64, vp, i64, vp, sz, vp]),
+            "nvfp4_attention_paged_scratch_bytes": (sz, [i32, i32, i32]),
+            "nvfp4_attention_decode_paged": (C.c_int, [vp, i64, i64, i32, i32, T, T, i32, vp, i64, i32,
+                                                       vp, i32, C.c_float, vp, i64, i64, vp, vp, sz,
+                                                       vp, sz, vp]),
         }
         for name, (res, args) in sig.items():
             f = getattr(L, name)
@@ -394,6 +411,217 @@ def nvfp4_attention_decode(q: torch.Tensor, k: NVFP4Tensor, v: NVFP4Tensor, head
                                         heads_kv, float(scale), out.data_ptr(), out.stride(0), ws.ptr,
                                         ws.nbytes, _stream(stream)), "nvfp4_attention_decode")
     return out
+
+
+# -------------------------------------------------------- paged KV cache
+def _require(ok: bool, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _together(device, **tensors):
+    """All of them are CUDA tensors of one device."""
+    for name, t in tensors.items():
+        _require(t is None or (t.is_cuda and t.device == device),
+                 f"{name} is not on {device}, the device of the first argument")
+
+
+@contextlib.contextmanager
+def _switched(device, stream):
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _on(device, stream):
+    """The tensors' device and the given stream made current, so that outputs
+    and scratch belong to the stream the kernels run on."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return _switched(device, stream)
+
+
+def _check_pool(k: NVFP4Tensor, v: NVFP4Tensor):
+    """The buffers hold what the C ABI is told (it cannot see their sizes)."""
+    for name, t in (("k_cache", k), ("v_cache", v)):
+        codes, scales = t.codes, t.scales
+        _require(t.layout == SF_LINEAR, f"{name}: the cache needs the linear scale layout")
+        _require(codes.dtype == torch.uint8 and codes.is_contiguous()
+                 and codes.numel() == t.rows * (t.cols // 2), f"{name}.codes: uint8 [rows, cols / 2]")
+        _require(scales.dtype == torch.uint8 and scales.is_contiguous()
+                 and scales.numel() == t.rows * (t.cols // 16), f"{name}.scales: uint8, rows * cols / 16")
+        _require(t.global_scale.dtype == torch.float32 and t.global_scale.numel() == 1,
+                 f"{name}.global_scale: float32, one element")
+        _together(k.codes.device, **{name + ".codes": codes, name + ".scales": scales,
+                                     name + ".global_scale": t.global_scale})
+
+
+def _check_rope(device, positions, table, tokens):
+    _require(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2
+             and table.is_contiguous(), "table: float32 [positions, rotary_dim / 2, 2], contiguous")
+    _require(positions is not None and positions.dtype == torch.int32 and positions.dim() == 1
+             and positions.is_contiguous() and positions.numel() == tokens,
+             "positions: int32 [tokens], contiguous")
+    _together(device, table=table, positions=positions)
+
+
+def nvfp4_rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "plain",
+                        factor: float = 1.0, original_positions: float = 0.0, low: float = 1.0,
+                        high: float = 32.0) -> torch.Tensor:
+    """Rotary frequencies, float64 [rotary_dim / 2] on the host.  ``scaling``:
+    plain, linear, ntk, bands or ramp (see nvfp4_rope_inv_freq in the header)."""
+    _require(scaling in ROPE_SCALINGS, f"scaling: one of {', '.join(ROPE_SCALINGS)}")
+    out = torch.empty(max(int(rotary_dim) // 2, 0), dtype=torch.float64)
+    _check(lib().nvfp4_rope_inv_freq(rotary_dim, base, ROPE_SCALINGS[scaling], factor,
+                                     original_positions, low, high, out.data_ptr()),
+           "nvfp4_rope_inv_freq")
+    return out
+
+
+def nvfp4_rope_table(inv_freq: torch.Tensor, positions: int, magnitude: float = 1.0, first: int = 0,
+                     device="cuda", stream=None) -> torch.Tensor:
+    """(cos, sin) * magnitude of positions first .. first + positions - 1:
+    float32 [positions, rotary_dim / 2, 2], the ``table`` of nvfp4_rope and
+    nvfp4_kv_write."""
+    _require(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1, "inv_freq: float64, one dimension")
+    device = inv_freq.device if inv_freq.is_cuda else torch.device(device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    with _on(device, stream):
+        f = inv_freq.to(device).contiguous()
+        out = torch.empty((positions, f.numel(), 2), dtype=torch.float32, device=device)
+        _check(lib().nvfp4_rope_table(f.data_ptr(), 2 * f.numel(), first, positions, magnitude,
+                                      out.data_ptr(), _stream(None)), "nvfp4_rope_table")
+    return out
+
+
+def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
+               inverse: bool = False, out: torch.Tensor | None = None,
+               workspace: Workspace | None = None, stream=None) -> torch.Tensor:
+    """Rotary positions of a BF16 tensor [tokens, heads, head_dim] (any token
+    and head strides): the first 2 * table.shape[1] values of each head are
+    rotated, the rest copied.  ``inverse`` gives the gradient of x from that
+    of the output.  ``out`` may be x itself; tokens at position -1 keep what
+    ``out`` holds there."""
+    _require(x.dtype == torch.bfloat16 and x.dim() == 3 and x.is_cuda
+             and (x.stride(2) == 1 or x.shape[2] == 1), "x: BF16 CUDA [tokens, heads, head_dim], innermost contiguous")
+    tokens, heads, dim = x.shape
+    _check_rope(x.device, positions, table, tokens)
+    _together(x.device, out=out)
+    with _on(x.device, stream):
+        if out is None:
+            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=x.device)
+        _require(out.dtype == torch.bfloat16 and out.shape == x.shape
+                 and (out.stride(2) == 1 or dim == 1), "out: BF16 of x's shape, innermost contiguous")
+        ws = workspace or default_workspace(x.device)
+        _check(lib().nvfp4_rope(x.data_ptr(), x.stride(0), x.stride(1), tokens, heads, dim,
+                                positions.data_ptr(), table.data_ptr(), table.shape[0],
+                                2 * table.shape[1], int(interleaved), int(inverse), out.data_ptr(),
+                                out.stride(0), out.stride(1), ws.ptr, ws.nbytes, _stream(None)),
+               "nvfp4_rope")
+    return out
+
+
+def nvfp4_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: NVFP4Tensor,
+                   v_cache: NVFP4Tensor, positions: torch.Tensor | None = None,
+                   table: torch.Tensor | None = None, interleaved: bool = False,
+                   workspace: Workspace | None = None, stream=None) -> None:
+    """Quantize k and v (BF16 [tokens, heads, head_dim]) into rows ``slots``
+    (int32, -1 = none) of the cache, under the caches' own tensor scales.
+    With a ``table`` the keys are rotated to ``positions`` first."""
+    for name, t in (("k", k), ("v", v)):
+        _require(t.dtype == torch.bfloat16 and t.dim() == 3 and t.is_cuda and t.shape == k.shape
+                 and (t.stride(2) == 1 or t.shape[2] == 1),
+                 f"{name}: BF16 CUDA [tokens, heads, head_dim], innermost contiguous")
+    tokens, heads, dim = k.shape
+    _require(slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous()
+             and slots.numel() == tokens, "slots: int32 [tokens], contiguous")
+    _check_pool(k_cache, v_cache)
+    _together(k.device, v=v, slots=slots, k_cache=k_cache.codes)
+    if table is not None:
+        _check_rope(k.device, positions, table, tokens)
+    with _on(k.device, stream):
+        ws = workspace or default_workspace(k.device)
+        tk, tv = k_cache.c_struct(), v_cache.c_struct()
+        _check(lib().nvfp4_kv_write(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
+                                    v.stride(1), tokens, heads, dim, slots.data_ptr(), C.byref(tk),
+                                    C.byref(tv), _ptr(positions if table is not None else None), _ptr(table),
+                                    0 if table is None else table.shape[0],
+                                    0 if table is None else 2 * table.shape[1], int(interleaved),
+                                    ws.ptr, ws.nbytes, _stream(None)), "nvfp4_kv_write")
+
+
+def nvfp4_kv_read(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, slots: torch.Tensor,
+                  out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                  workspace: Workspace | None = None, stream=None):
+    """Rows ``slots`` (int32, -1 = zeros) of the cache as BF16 [rows, heads *
+    head_dim] pairs (k, v), restored as nvfp4_dequantize restores them."""
+    _require(slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous() and slots.is_cuda,
+             "slots: int32 CUDA [rows], contiguous")
+    _check_pool(k_cache, v_cache)
+    rows, cols = slots.numel(), k_cache.cols
+    _together(slots.device, k_cache=k_cache.codes)
+    with _on(slots.device, stream):
+        if out is None:
+            out = tuple(torch.empty((rows, cols), dtype=torch.bfloat16, device=slots.device) for _ in range(2))
+        for t in out:
+            _require(t.dtype == torch.bfloat16 and t.shape == (rows, cols) and (t.stride(1) == 1 or cols == 1),
+                     "out: two BF16 [rows, heads * head_dim], innermost contiguous")
+            _together(slots.device, out=t)
+        ws = workspace or default_workspace(slots.device)
+        tk, tv = k_cache.c_struct(), v_cache.c_struct()
+        _check(lib().nvfp4_kv_read(C.byref(tk), C.byref(tv), slots.data_ptr(), rows, out[0].data_ptr(),
+                                   out[0].stride(0), out[1].data_ptr(), out[1].stride(0), ws.ptr,
+                                   ws.nbytes, _stream(None)), "nvfp4_kv_read")
+    return out
+
+
+def nvfp4_attention_decode_paged(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor,
+                                 heads_kv: int, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                                 page_size: int, scale: float | None = None,
+                                 out: torch.Tensor | None = None, return_lse: bool = False,
+                                 workspace: Workspace | None = None, stream=None):
+    """Decode attention of a batch over the paged cache: q BF16 [sequences,
+    heads_q, head_dim], block_table int32 [sequences, pages], seq_lens int32
+    [sequences].  Returns BF16 of q's shape, with ``return_lse`` also the
+    float32 [sequences, heads_q] log of the summed exponentials.  The softmax
+    scale defaults to 1 / sqrt(head_dim)."""
+    _require(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_cuda and q.stride(2) == 1,
+             "q: BF16 CUDA [sequences, heads_q, head_dim], innermost contiguous")
+    sequences, heads_q, dim = q.shape
+    _check_pool(k_cache, v_cache)
+    _require(heads_kv > 0 and k_cache.cols == heads_kv * dim, "the cache's columns are heads_kv * head_dim")
+    _require(block_table.dtype == torch.int32 and block_table.dim() == 2
+             and block_table.shape[0] == sequences and (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
+             "block_table: int32 [sequences, pages], innermost contiguous")
+    _require(seq_lens.dtype == torch.int32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
+             and seq_lens.numel() == sequences, "seq_lens: int32 [sequences], contiguous")
+    _together(q.device, k_cache=k_cache.codes, block_table=block_table, seq_lens=seq_lens, out=out)
+    if scale is None:
+        scale = dim ** -0.5
+    with _on(q.device, stream):
+        if out is None:
+            out = torch.empty((sequences, heads_q, dim), dtype=torch.bfloat16, device=q.device)
+        _require(out.dtype == torch.bfloat16 and out.shape == q.shape and out.stride(2) == 1,
+                 "out: BF16 of q's shape, innermost contiguous")
+        lse = torch.empty((sequences, heads_q), dtype=torch.float32, device=q.device) if return_lse else None
+        # scratch of the call's own, from the allocator of the stream (or the
+        # graph being captured): calls on two streams do not share it
+        need = int(lib().nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, dim))
+        scratch = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        ws = workspace or default_workspace(q.device)
+        tk, tv = k_cache.c_struct(), v_cache.c_struct()
+        _check(lib().nvfp4_attention_decode_paged(
+            q.data_ptr(), q.stride(0), q.stride(1), sequences, heads_q, C.byref(tk), C.byref(tv), heads_kv,
+            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
+            page_size, float(scale), out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), ws.ptr,
+            ws.nbytes, _ptr(scratch), need, _stream(None)), "nvfp4_attention_decode_paged")
+    return (out, lse) if return_lse else out
 
 
 def nvfp4_quantize_swiglu(gate_up: torch.Tensor, out: NVFP4Tensor | None = None,

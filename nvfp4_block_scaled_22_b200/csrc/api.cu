@@ -2,6 +2,7 @@
 // Argument validation, device check, tensor-map encoding and launches.
 // No device memory is allocated here; every buffer belongs to the caller.
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -296,6 +297,37 @@ nvfp4_status check_transposed(const void *x, int64_t ld, const nvfp4_tensor *out
     }
     return check_workspace(workspace, workspace_bytes,
                            nvfp4_workspace_bytes(NVFP4_OP_QUANTIZE, out->rows, out->cols, 0, 0));
+}
+
+// True when rows of `inner` elements at strides (sa, sb) over na x nb do not
+// overlap (a written array must hold each row once).
+bool rows_apart(int64_t sa, int64_t na, int64_t sb, int64_t nb, int64_t inner) {
+    if (na > 1 && sa < inner) return false;
+    if (nb > 1 && sb < inner) return false;
+    if (na <= 1 || nb <= 1) return true;
+    // one axis steps past everything the other covers
+    return sa <= sb ? (na - 1) <= (sb - inner) / sa : (nb - 1) <= (sa - inner) / sb;
+}
+
+// Checks shared by the rotary arguments of nvfp4_rope and nvfp4_kv_write.
+nvfp4_status check_rope(const int32_t *d_positions, const float *d_table, int64_t table_rows,
+                        int32_t rotary_dim, int32_t interleaved, int32_t head_dim) {
+    if (d_positions == nullptr || table_rows < 1) return NVFP4_ERR_INVALID_ARG;
+    if (interleaved != 0 && interleaved != 1) return NVFP4_ERR_INVALID_ARG;
+    if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > head_dim) return NVFP4_ERR_SHAPE;
+    if ((reinterpret_cast<uintptr_t>(d_positions) & 3u) != 0 || !aligned16(d_table)) return NVFP4_ERR_ALIGNMENT;
+    return NVFP4_OK;
+}
+
+// A cache pool: LINEAR scales, K and V of equal shape.
+nvfp4_status check_pools(const nvfp4_tensor *K, const nvfp4_tensor *V) {
+    nvfp4_status st = check_tensor(K);
+    if (st != NVFP4_OK) return st;
+    st = check_tensor(V);
+    if (st != NVFP4_OK) return st;
+    if (K->sf_layout != NVFP4_SF_LINEAR || V->sf_layout != NVFP4_SF_LINEAR) return NVFP4_ERR_SHAPE;
+    if (K->rows != V->rows || K->cols != V->cols) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
 }
 
 }  // namespace
@@ -719,6 +751,310 @@ nvfp4_status nvfp4_attention_decode(const void *q, int64_t ldq, int32_t heads_q,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return launched(cudaLaunchKernelEx(&cfg, k_attn_combine, p));
+}
+
+nvfp4_status nvfp4_rope_inv_freq(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                 double original_positions, double low, double high,
+                                 double *inv_freq) {
+    if (inv_freq == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (rotary_dim < 2 || rotary_dim % 2 != 0) return NVFP4_ERR_SHAPE;
+    if (scaling < NVFP4_ROPE_PLAIN || scaling > NVFP4_ROPE_RAMP) return NVFP4_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !std::isfinite(base)) return NVFP4_ERR_INVALID_ARG;
+    if (scaling != NVFP4_ROPE_PLAIN && (!(factor > 0.0) || !std::isfinite(factor))) return NVFP4_ERR_INVALID_ARG;
+    if (scaling == NVFP4_ROPE_NTK && rotary_dim < 4) return NVFP4_ERR_SHAPE;
+    const bool mixed = scaling == NVFP4_ROPE_BANDS || scaling == NVFP4_ROPE_RAMP;
+    if (mixed && (!(original_positions > 0.0) || !std::isfinite(original_positions) || !(low > 0.0) ||
+                  !(high > low) || !std::isfinite(high)))
+        return NVFP4_ERR_INVALID_ARG;
+    const double two_pi = 6.283185307179586476925286766559;
+    const int32_t pairs = rotary_dim / 2;
+    if (scaling == NVFP4_ROPE_NTK) base *= std::pow(factor, (double)rotary_dim / (rotary_dim - 2));
+    double first = 0.0, last = 0.0;                      // NVFP4_ROPE_RAMP: pairs between which the ramp runs
+    if (scaling == NVFP4_ROPE_RAMP) {
+        const double per = pairs / std::log(base);
+        first = std::fmax(std::floor(per * std::log(original_positions / (two_pi * high))), 0.0);
+        last = std::fmin(std::ceil(per * std::log(original_positions / (two_pi * low))), rotary_dim - 1.0);
+        if (last <= first) last = first + 0.001;
+    }
+    for (int32_t i = 0; i < pairs; ++i) {
+        const double f = std::pow(base, -2.0 * i / rotary_dim);
+        double kept = 1.0;                               // share of the unscaled frequency
+        if (scaling == NVFP4_ROPE_LINEAR) kept = 0.0;
+        if (scaling == NVFP4_ROPE_BANDS)
+            kept = std::fmin(std::fmax((original_positions * f / two_pi - low) / (high - low), 0.0), 1.0);
+        if (scaling == NVFP4_ROPE_RAMP)
+            kept = 1.0 - std::fmin(std::fmax((i - first) / (last - first), 0.0), 1.0);
+        inv_freq[i] = kept * f + (kept < 1.0 ? (1.0 - kept) * (f / factor) : 0.0);
+    }
+    return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_rope_table(const double *d_inv_freq, int32_t rotary_dim, int64_t first_position,
+                              int64_t rows, double magnitude, float *d_table, void *stream) {
+    if (rotary_dim < 2 || rotary_dim % 2 != 0) return NVFP4_ERR_SHAPE;
+    if (rows < 0 || first_position < 0 || rows > INT32_MAX || first_position > INT32_MAX - rows)
+        return NVFP4_ERR_INVALID_ARG;
+    if (!std::isfinite(magnitude)) return NVFP4_ERR_INVALID_ARG;
+    if (rows == 0) return NVFP4_OK;
+    if (d_inv_freq == nullptr || d_table == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(d_inv_freq) & 7u) != 0 || !aligned16(d_table)) return NVFP4_ERR_ALIGNMENT;
+    int sms = 0;
+    nvfp4_status st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    const int64_t n = rows * (rotary_dim / 2);
+    const int grid = (int)std::min<int64_t>(ceil_div(n, 256), 8LL * sms);
+    k_rope_table<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
+        d_inv_freq, rotary_dim / 2, first_position, n, magnitude, reinterpret_cast<float2 *>(d_table));
+    return launched(cudaGetLastError());
+}
+
+nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, int64_t tokens,
+                        int32_t heads, int32_t head_dim, const int32_t *d_positions,
+                        const float *d_table, int64_t table_rows, int32_t rotary_dim,
+                        int32_t interleaved, int32_t inverse, void *y, int64_t y_token_stride,
+                        int64_t y_head_stride, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    if (tokens < 0 || heads < 0 || head_dim < 0 || x_token_stride < 0 || x_head_stride < 0 ||
+        y_token_stride < 0 || y_head_stride < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (inverse != 0 && inverse != 1) return NVFP4_ERR_INVALID_ARG;
+    if (rotary_dim < 2 || rotary_dim % 2 != 0 || rotary_dim > head_dim) return NVFP4_ERR_SHAPE;
+    nvfp4_status st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != NVFP4_OK) return st;
+    if (tokens == 0 || heads == 0) return NVFP4_OK;
+    if (x == nullptr || y == nullptr || d_table == nullptr) return NVFP4_ERR_INVALID_ARG;
+    st = check_rope(d_positions, d_table, table_rows, rotary_dim, interleaved, head_dim);
+    if (st != NVFP4_OK) return st;
+    if (((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 1u) != 0) return NVFP4_ERR_ALIGNMENT;
+    if (!rows_apart(y_token_stride, tokens, y_head_stride, heads, head_dim)) return NVFP4_ERR_SHAPE;
+    const bool in_place = x == y;
+    if (in_place && ((tokens > 1 && x_token_stride != y_token_stride) ||
+                     (heads > 1 && x_head_stride != y_head_stride)))
+        return NVFP4_ERR_INVALID_ARG;
+    const int32_t pairs = rotary_dim / 2, rest = in_place ? 0 : head_dim - rotary_dim;
+    const bool pieces = aligned16(x) && aligned16(y) &&
+                        (x_token_stride | x_head_stride | y_token_stride | y_head_stride) % 8 == 0 &&
+                        rest % 8 == 0 && (interleaved ? pairs % 4 == 0 : pairs % 8 == 0);
+    const int64_t per_head = !pieces ? pairs + rest
+                                     : (interleaved ? (rotary_dim + rest) / 8 : pairs / 8 + rest / 8);
+    // items are counted in 31 bits
+    if (tokens > INT32_MAX / per_head / heads) return NVFP4_ERR_SHAPE;
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    RopeParams p;
+    p.x = static_cast<const uint16_t *>(x);
+    p.xs_t = x_token_stride;
+    p.xs_h = x_head_stride;
+    p.y = static_cast<uint16_t *>(y);
+    p.ys_t = y_token_stride;
+    p.ys_h = y_head_stride;
+    p.positions = d_positions;
+    p.table = reinterpret_cast<const float2 *>(d_table);
+    p.table_rows = table_rows;
+    p.pairs = pairs;
+    p.dim = head_dim;
+    p.sign = inverse ? -1.0f : 1.0f;
+    p.items = (uint32_t)(tokens * heads * per_head);
+    p.per_token = fast_div((uint32_t)(heads * per_head));
+    p.per_head = fast_div((uint32_t)per_head);
+    p.status = static_cast<uint32_t *>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!pieces)
+        k_rope_any<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p, interleaved, rest > 0);
+    else if (interleaved)
+        k_rope_interleaved<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+    else
+        k_rope_half<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+    return launched(cudaGetLastError());
+}
+
+nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_head_stride,
+                            const void *v, int64_t v_token_stride, int64_t v_head_stride,
+                            int64_t tokens, int32_t heads, int32_t head_dim, const int32_t *d_slots,
+                            const nvfp4_tensor *K, const nvfp4_tensor *V, const int32_t *d_positions,
+                            const float *d_table, int64_t table_rows, int32_t rotary_dim,
+                            int32_t interleaved, void *workspace, size_t workspace_bytes,
+                            void *stream) {
+    nvfp4_status st = check_pools(K, V);
+    if (st != NVFP4_OK) return st;
+    if (tokens < 0 || heads < 1 || head_dim < 1 || k_token_stride < 0 || k_head_stride < 0 ||
+        v_token_stride < 0 || v_head_stride < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    if (head_dim % 16 != 0 || K->cols != (int64_t)heads * head_dim) return NVFP4_ERR_SHAPE;
+    st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != NVFP4_OK) return st;
+    if (d_table != nullptr) {
+        st = check_rope(d_positions, d_table, table_rows, rotary_dim, interleaved, head_dim);
+        if (st != NVFP4_OK) return st;
+    }
+    if (tokens == 0) return NVFP4_OK;
+    if (k == nullptr || v == nullptr || d_slots == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(d_slots) & 3u) != 0 ||
+        (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    const int64_t row_blocks = K->cols / 16;
+    if (tokens > INT32_MAX / (2 * row_blocks)) return NVFP4_ERR_SHAPE;      // items are counted in 31 bits
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    KvWriteParams p;
+    p.k = static_cast<const uint16_t *>(k);
+    p.v = static_cast<const uint16_t *>(v);
+    p.ks_t = k_token_stride;
+    p.ks_h = k_head_stride;
+    p.vs_t = v_token_stride;
+    p.vs_h = v_head_stride;
+    p.slots = d_slots;
+    p.pool_rows = K->rows;
+    p.kc = static_cast<uint8_t *>(K->codes);
+    p.ks = static_cast<uint8_t *>(K->scales);
+    p.vc = static_cast<uint8_t *>(V->codes);
+    p.vs = static_cast<uint8_t *>(V->scales);
+    p.gk = K->global;
+    p.gv = V->global;
+    p.row_codes = K->cols / 2;
+    p.row_scales = row_blocks;
+    p.positions = d_positions;
+    p.table = reinterpret_cast<const float2 *>(d_table);
+    p.table_rows = table_rows;
+    p.pairs = rotary_dim / 2;
+    p.interleaved = interleaved;
+    p.items = (uint32_t)(tokens * 2 * row_blocks);
+    p.per_token = fast_div((uint32_t)(2 * row_blocks));
+    p.per_head = fast_div((uint32_t)(head_dim / 16));
+    p.status = static_cast<uint32_t *>(workspace);
+    const unsigned grid = (unsigned)ceil_div(p.items, 256);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d_table == nullptr)
+        k_kv_write<<<grid, 256, 0, s>>>(p);
+    else if (!interleaved && p.pairs % 16 == 0)
+        k_kv_write_half<<<grid, 256, 0, s>>>(p);
+    else
+        k_kv_write_any<<<grid, 256, 0, s>>>(p);
+    return launched(cudaGetLastError());
+}
+
+nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V, const int32_t *d_slots,
+                           int64_t rows, void *k, int64_t ldk, void *v, int64_t ldv, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    nvfp4_status st = check_pools(K, V);
+    if (st != NVFP4_OK) return st;
+    if (rows < 0) return NVFP4_ERR_INVALID_ARG;
+    st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != NVFP4_OK) return st;
+    if (rows == 0 || K->cols == 0) return NVFP4_OK;
+    if (k == nullptr || v == nullptr || d_slots == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(d_slots) & 3u) != 0 ||
+        ldk % 8 != 0 || ldv % 8 != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    if (ldk < K->cols || ldv < K->cols) return NVFP4_ERR_SHAPE;
+    const int64_t row_blocks = K->cols / 16;
+    if (rows > INT32_MAX / (2 * row_blocks)) return NVFP4_ERR_SHAPE;        // items are counted in 31 bits
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    KvReadParams p;
+    p.kc = static_cast<const uint8_t *>(K->codes);
+    p.ks = static_cast<const uint8_t *>(K->scales);
+    p.vc = static_cast<const uint8_t *>(V->codes);
+    p.vs = static_cast<const uint8_t *>(V->scales);
+    p.gk = K->global;
+    p.gv = V->global;
+    p.pool_rows = K->rows;
+    p.row_codes = K->cols / 2;
+    p.row_scales = row_blocks;
+    p.slots = d_slots;
+    p.yk = static_cast<uint16_t *>(k);
+    p.yv = static_cast<uint16_t *>(v);
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.vec32 = (((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 31u) == 0 &&
+               (ldk | ldv) % 16 == 0) ? 1 : 0;
+    p.items = (uint32_t)(rows * 2 * row_blocks);
+    p.per_row = fast_div((uint32_t)(2 * row_blocks));
+    p.row_blocks = (uint32_t)row_blocks;
+    p.status = static_cast<uint32_t *>(workspace);
+    k_kv_read<<<(unsigned)ceil_div(p.items, 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    return launched(cudaGetLastError());
+}
+
+size_t nvfp4_attention_paged_scratch_bytes(int32_t heads_q, int32_t heads_kv, int32_t head_dim) {
+    (void)heads_q;
+    (void)heads_kv;
+    (void)head_dim;
+    return 0;
+}
+
+nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, int64_t q_head_stride,
+                                          int32_t sequences, int32_t heads_q, const nvfp4_tensor *K,
+                                          const nvfp4_tensor *V, int32_t heads_kv,
+                                          const int32_t *d_block_table, int64_t table_stride,
+                                          int32_t table_pages, const int32_t *d_seq_lens,
+                                          int32_t page_size, float scale, void *o,
+                                          int64_t o_seq_stride, int64_t o_head_stride, float *d_lse,
+                                          void *workspace, size_t workspace_bytes, void *scratch,
+                                          size_t scratch_bytes, void *stream) {
+    nvfp4_status st = check_pools(K, V);
+    if (st != NVFP4_OK) return st;
+    if (sequences < 0 || heads_q < 1 || heads_kv < 1 || table_pages < 0 || table_stride < 0 ||
+        page_size < 1 || q_seq_stride < 0 || q_head_stride < 0 || o_seq_stride < 0 ||
+        o_head_stride < 0 || !std::isfinite(scale))
+        return NVFP4_ERR_INVALID_ARG;
+    if (heads_q % heads_kv != 0 || K->cols % heads_kv != 0) return NVFP4_ERR_SHAPE;
+    const int64_t dim = K->cols / heads_kv;
+    if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_SHAPE;
+    if (K->rows % page_size != 0 || K->rows > INT32_MAX) return NVFP4_ERR_SHAPE;
+    if ((int64_t)table_pages * page_size > INT32_MAX) return NVFP4_ERR_SHAPE;
+    if (sequences > 1 && table_stride < table_pages) return NVFP4_ERR_SHAPE;
+    st = check_workspace(workspace, workspace_bytes, kStatusBytes);
+    if (st != NVFP4_OK) return st;
+    const size_t need = nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, (int32_t)dim);
+    if (need > 0) {
+        st = check_workspace(scratch, scratch_bytes, need);
+        if (st != NVFP4_OK) return st;
+    }
+    if (sequences == 0) return NVFP4_OK;
+    if (q == nullptr || o == nullptr || d_seq_lens == nullptr || (table_pages > 0 && d_block_table == nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(o) ||
+        (q_seq_stride | q_head_stride | o_seq_stride | o_head_stride) % 8 != 0 ||
+        ((reinterpret_cast<uintptr_t>(d_block_table) | reinterpret_cast<uintptr_t>(d_seq_lens) |
+          reinterpret_cast<uintptr_t>(d_lse)) & 3u) != 0)
+        return NVFP4_ERR_ALIGNMENT;
+    if (!rows_apart(o_seq_stride, sequences, o_head_stride, heads_q, dim)) return NVFP4_ERR_SHAPE;
+    int sms = 0;
+    st = current_device(&sms);
+    if (st != NVFP4_OK) return st;
+    PagedAttnParams p;
+    p.q = static_cast<const uint16_t *>(q);
+    p.qs_b = q_seq_stride;
+    p.qs_h = q_head_stride;
+    p.kc = static_cast<const uint8_t *>(K->codes);
+    p.ks = static_cast<const uint8_t *>(K->scales);
+    p.vc = static_cast<const uint8_t *>(V->codes);
+    p.vs = static_cast<const uint8_t *>(V->scales);
+    p.gk = K->global;
+    p.gv = V->global;
+    p.row_codes = K->cols / 2;
+    p.row_scales = K->cols / 16;
+    p.block_table = d_block_table;
+    p.table_stride = table_stride;
+    p.table_pages = table_pages;
+    p.n_pages = (int32_t)(K->rows / page_size);
+    p.seq_lens = d_seq_lens;
+    p.sequences = sequences;
+    p.heads_q = heads_q;
+    p.heads_kv = heads_kv;
+    p.group = heads_q / heads_kv;
+    p.page_size = page_size;
+    p.scale = scale;
+    p.o = static_cast<uint16_t *>(o);
+    p.os_b = o_seq_stride;
+    p.os_h = o_head_stride;
+    p.lse = d_lse;
+    p.status = static_cast<uint32_t *>(workspace);
+    return launched(launch_paged_attention(p, (int)dim, static_cast<cudaStream_t>(stream)));
 }
 
 nvfp4_status nvfp4_quantize_swiglu(const void *gate_up, int64_t ld, const nvfp4_tensor *out,

@@ -193,4 +193,101 @@ struct AttnParams {
 __global__ void k_attn_partial(AttnParams p);
 __global__ void k_attn_combine(AttnParams p);
 
+// Division of n < 2^31 by a launch constant d >= 1: n / d =
+// (hi32(n m) + n) >> s with s = ceil(log2 d), m = floor(2^32 (2^s - d) / d) + 1
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994; for n < 2^31 the sum stays below 2^32).
+struct FastDiv {
+    uint32_t d, m, s;
+};
+inline FastDiv fast_div(uint32_t d) {
+    FastDiv f;
+    f.d = d;
+    f.s = 0;
+    while (f.s < 31 && (1u << f.s) < d) ++f.s;
+    f.m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << f.s) - d)) / d + 1);
+    return f;
+}
+
+// Rotary positions (rope.cu).
+struct RopeParams {
+    const uint16_t *x;       // BF16, strides in elements
+    int64_t xs_t, xs_h;
+    uint16_t *y;
+    int64_t ys_t, ys_h;
+    const int32_t *positions;
+    const float2 *table;     // [table_rows][pairs] (cos, sin)
+    int64_t table_rows;
+    int32_t pairs, dim;
+    float sign;              // +1, or -1 for the inverse
+    uint32_t items;          // work items (tokens x heads x items of a head)
+    FastDiv per_token, per_head;
+    uint32_t *status;
+};
+constexpr int kRopeItems = 4;   // items a thread takes, 256 apart
+__global__ void k_rope_table(const double *inv_freq, int32_t pairs, int64_t first, int64_t n,
+                             double magnitude, float2 *table);
+__global__ void k_rope_half(RopeParams p);
+__global__ void k_rope_interleaved(RopeParams p);
+__global__ void k_rope_any(RopeParams p, int interleaved, int with_rest);
+
+// Paged cache write and read (kv_cache.cu).
+struct KvWriteParams {
+    const uint16_t *k, *v;   // BF16 [tokens][heads][dim], strides in elements
+    int64_t ks_t, ks_h, vs_t, vs_h;
+    const int32_t *slots;    // [tokens] pool rows, -1 = none
+    int64_t pool_rows;
+    uint8_t *kc, *ks, *vc, *vs;
+    const float *gk, *gv;
+    int64_t row_codes, row_scales;
+    const int32_t *positions;
+    const float2 *table;     // nullptr: keys are not rotated
+    int64_t table_rows;
+    int32_t pairs;
+    int32_t interleaved;
+    uint32_t items;          // tokens x (blocks of a K row + blocks of a V row)
+    FastDiv per_token;       // 2 x blocks of a row
+    FastDiv per_head;        // blocks of a head
+    uint32_t *status;
+};
+__global__ void k_kv_write(KvWriteParams p);
+__global__ void k_kv_write_half(KvWriteParams p);
+__global__ void k_kv_write_any(KvWriteParams p);
+
+struct KvReadParams {
+    const uint8_t *kc, *ks, *vc, *vs;
+    const float *gk, *gv;
+    int64_t pool_rows, row_codes, row_scales;
+    const int32_t *slots;
+    uint16_t *yk, *yv;       // BF16 [rows][cols], pitches in elements
+    int64_t ldk, ldv;
+    int32_t vec32;           // both outputs allow 32-byte stores
+    uint32_t items;          // rows x (blocks of a K row + blocks of a V row)
+    FastDiv per_row;
+    uint32_t row_blocks;
+    uint32_t *status;
+};
+__global__ void k_kv_read(KvReadParams p);
+
+// Decode attention over a paged cache (attention_paged.cu).
+struct PagedAttnParams {
+    const uint16_t *q;       // BF16 [sequences][heads_q][dim], strides in elements
+    int64_t qs_b, qs_h;
+    const uint8_t *kc, *ks, *vc, *vs;
+    const float *gk, *gv;
+    int64_t row_codes, row_scales;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_pages;     // pages a sequence can have
+    int32_t n_pages;         // pages of the pool
+    const int32_t *seq_lens;
+    int32_t sequences, heads_q, heads_kv, group, page_size;
+    float scale;
+    uint16_t *o;
+    int64_t os_b, os_h;
+    float *lse;              // nullptr, or [sequences][heads_q]
+    uint32_t *status;
+};
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int dim, cudaStream_t s);
+
 }  // namespace nvfp4
