@@ -980,10 +980,10 @@ nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V, const i
 }
 
 size_t nvfp4_attention_paged_scratch_bytes(int32_t heads_q, int32_t heads_kv, int32_t head_dim) {
-    (void)heads_q;
-    (void)heads_kv;
-    (void)head_dim;
-    return 0;
+    if (heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0 ||
+        (head_dim != 64 && head_dim != 128 && head_dim != 256))
+        return 0;
+    return paged_scratch_bytes(paged_plan(heads_q, heads_kv, head_dim), head_dim);
 }
 
 nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, int64_t q_head_stride,
@@ -1005,15 +1005,14 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     const int64_t dim = K->cols / heads_kv;
     if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_SHAPE;
     if (K->rows % page_size != 0 || K->rows > INT32_MAX) return NVFP4_ERR_SHAPE;
-    if ((int64_t)table_pages * page_size > INT32_MAX) return NVFP4_ERR_SHAPE;
+    // token numbers, and those of a last tile's empty places, are counted in 31 bits
+    if ((int64_t)table_pages * page_size > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
     if (sequences > 1 && table_stride < table_pages) return NVFP4_ERR_SHAPE;
     st = check_workspace(workspace, workspace_bytes, kStatusBytes);
     if (st != NVFP4_OK) return st;
-    const size_t need = nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, (int32_t)dim);
-    if (need > 0) {
-        st = check_workspace(scratch, scratch_bytes, need);
-        if (st != NVFP4_OK) return st;
-    }
+    const PagedPlan plan = paged_plan(heads_q, heads_kv, (int)dim);
+    st = check_workspace(scratch, scratch_bytes, paged_scratch_bytes(plan, (int)dim));
+    if (st != NVFP4_OK) return st;
     if (sequences == 0) return NVFP4_OK;
     if (q == nullptr || o == nullptr || d_seq_lens == nullptr || (table_pages > 0 && d_block_table == nullptr))
         return NVFP4_ERR_INVALID_ARG;
@@ -1040,21 +1039,29 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     p.row_scales = K->cols / 16;
     p.block_table = d_block_table;
     p.table_stride = table_stride;
-    p.table_pages = table_pages;
+    p.capacity = table_pages * page_size;
     p.n_pages = (int32_t)(K->rows / page_size);
     p.seq_lens = d_seq_lens;
     p.sequences = sequences;
     p.heads_q = heads_q;
-    p.heads_kv = heads_kv;
     p.group = heads_q / heads_kv;
     p.page_size = page_size;
+    p.page_div = fast_div((uint32_t)page_size);
+    p.units_head = plan.units_head;
+    p.units_cta = plan.units_cta;
+    p.tile_shift = plan.tile_shift;
+    p.min_tiles = kPagedMinTiles;
     p.scale = scale;
     p.o = static_cast<uint16_t *>(o);
     p.os_b = o_seq_stride;
     p.os_h = o_head_stride;
     p.lse = d_lse;
     p.status = static_cast<uint32_t *>(workspace);
-    return launched(launch_paged_attention(p, (int)dim, static_cast<cudaStream_t>(stream)));
+    const int64_t parts = (int64_t)2 * plan.ranges * plan.blocks * plan.units_cta;
+    p.joins = static_cast<int4 *>(scratch);
+    p.part_o = reinterpret_cast<float *>(p.joins + plan.ranges);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + parts * 8 * dim);
+    return launched(launch_paged_attention(p, (int)dim, plan, static_cast<cudaStream_t>(stream)), 2);
 }
 
 nvfp4_status nvfp4_quantize_swiglu(const void *gate_up, int64_t ld, const nvfp4_tensor *out,

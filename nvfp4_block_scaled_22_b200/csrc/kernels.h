@@ -1,6 +1,7 @@
 // Kernel parameter blocks and launch entry points shared by the host API
 // (api.cu) and the kernel files.  Internal to libnvfp4.so.
 #pragma once
+#include <algorithm>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -270,6 +271,33 @@ struct KvReadParams {
 __global__ void k_kv_read(KvReadParams p);
 
 // Decode attention over a paged cache (attention_paged.cu).
+//
+// The launch plan, by the head counts alone (so that the scratch does not
+// depend on lengths or device): units (a KV head with up to 8 query heads),
+// units a CTA takes, CTAs over the units and ranges of the tile list.
+constexpr int kPagedMaxRanges = 296;
+constexpr int kPagedMinTiles = 1;
+struct PagedPlan {
+    int units_head;          // units of a KV head
+    int units_cta, tile_shift, blocks, ranges;
+};
+inline PagedPlan paged_plan(int heads_q, int heads_kv, int dim) {
+    PagedPlan n;
+    n.units_head = (heads_q / heads_kv + 7) / 8;
+    const int units = heads_kv * n.units_head;
+    n.units_cta = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
+    n.tile_shift = n.units_cta == 4 ? 5 : n.units_cta == 2 ? 6 : 7;   // 16 tokens x 8 / units_cta warps
+    n.blocks = units / n.units_cta;
+    const int ctas = dim == 256 ? 148 : 296;                          // one wave of 148 SMs
+    n.ranges = ctas / n.blocks > 1 ? ctas / n.blocks : 1;
+    return n;
+}
+// Scratch: per range two parts (a sequence cut at its start, one cut at its
+// end) of each unit: 8 x dim values and 8 (m, l) pairs; then the joins.
+inline size_t paged_scratch_bytes(const PagedPlan &n, int dim) {
+    return (size_t)2 * n.ranges * n.blocks * n.units_cta * (8 * dim + 16) * 4 + (size_t)n.ranges * 16;
+}
+
 struct PagedAttnParams {
     const uint16_t *q;       // BF16 [sequences][heads_q][dim], strides in elements
     int64_t qs_b, qs_h;
@@ -278,16 +306,23 @@ struct PagedAttnParams {
     int64_t row_codes, row_scales;
     const int32_t *block_table;
     int64_t table_stride;
-    int32_t table_pages;     // pages a sequence can have
+    int32_t capacity;        // tokens that a sequence's table entries hold
     int32_t n_pages;         // pages of the pool
     const int32_t *seq_lens;
-    int32_t sequences, heads_q, heads_kv, group, page_size;
+    int32_t sequences, heads_q, group, page_size;
+    FastDiv page_div;
+    int32_t units_head, units_cta;
+    int32_t tile_shift;      // log2 of the tokens of a tile of the schedule
+    int32_t min_tiles;       // tiles a range has at least (but the last)
     float scale;
     uint16_t *o;
     int64_t os_b, os_h;
     float *lse;              // nullptr, or [sequences][heads_q]
+    float *part_o;           // [2 ranges][units][8 * dim], fragment order
+    float2 *part_ml;         // [2 ranges][units][8]
+    int4 *joins;             // (sequence, first range, parts): by sequence, or by range if there are more sequences
     uint32_t *status;
 };
-cudaError_t launch_paged_attention(const PagedAttnParams &p, int dim, cudaStream_t s);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, int dim, const PagedPlan &plan, cudaStream_t s);
 
 }  // namespace nvfp4
