@@ -139,6 +139,20 @@ nvfp4_status encode_codes_map(CUtensorMap *m, const void *codes, int64_t rows, i
     return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
+// Rows of `pitch` bytes as (byte of a piece, row, piece): boxes of one piece
+// of 16 rows in box_pieces neighbouring pieces.
+nvfp4_status encode_rows_map(CUtensorMap *m, const void *base, uint32_t piece, int64_t rows, int64_t pieces,
+                             int64_t pitch, uint32_t box_pieces, CUtensorMapSwizzle swizzle) {
+    cuuint64_t dims[3] = {piece, (cuuint64_t)rows, (cuuint64_t)pieces};
+    cuuint64_t strides[2] = {(cuuint64_t)pitch, piece};
+    cuuint32_t box[3] = {piece, 16, box_pieces};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box,
+                          estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
 // Launch a kernel with programmatic stream serialization: it may be
 // scheduled while the previous kernel on the stream finishes, and waits on
 // the device (griddepcontrol.wait) before reading that kernel's results.
@@ -1004,7 +1018,7 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     if (heads_q % heads_kv != 0 || K->cols % heads_kv != 0) return NVFP4_ERR_SHAPE;
     const int64_t dim = K->cols / heads_kv;
     if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_SHAPE;
-    if (K->rows % page_size != 0 || K->rows > INT32_MAX) return NVFP4_ERR_SHAPE;
+    if (K->rows % page_size != 0 || K->rows > INT32_MAX || K->cols > INT32_MAX) return NVFP4_ERR_SHAPE;
     // token numbers, and those of a last tile's empty places, are counted in 31 bits
     if ((int64_t)table_pages * page_size > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
     if (sequences > 1 && table_stride < table_pages) return NVFP4_ERR_SHAPE;
@@ -1047,21 +1061,37 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     p.group = heads_q / heads_kv;
     p.page_size = page_size;
     p.page_div = fast_div((uint32_t)page_size);
-    p.units_head = plan.units_head;
-    p.units_cta = plan.units_cta;
-    p.tile_shift = plan.tile_shift;
+    p.plan = plan;
+    p.tma = page_size % 16 == 0 && p.row_scales % 16 == 0 && K->rows > 0;
     p.min_tiles = kPagedMinTiles;
+    p.timeout = g_timeout_cycles;
     p.scale = scale;
     p.o = static_cast<uint16_t *>(o);
     p.os_b = o_seq_stride;
     p.os_h = o_head_stride;
     p.lse = d_lse;
     p.status = static_cast<uint32_t *>(workspace);
-    const int64_t parts = (int64_t)2 * plan.ranges * plan.blocks * plan.units_cta;
+    const int64_t parts = (int64_t)2 * plan.ranges * plan.units;
     p.joins = static_cast<int4 *>(scratch);
     p.part_o = reinterpret_cast<float *>(p.joins + plan.ranges);
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + parts * 8 * dim);
-    return launched(launch_paged_attention(p, (int)dim, plan, static_cast<cudaStream_t>(stream)), 2);
+    PagedMaps maps = {};
+    if (p.tma) {
+        st = get_encode();
+        if (st != NVFP4_OK) return st;
+        const uint32_t heads = 1u << plan.heads_shift, codes = (uint32_t)dim / 2;
+        const uint32_t groups = std::max<uint32_t>(1u, heads * (uint32_t)(dim / 16) / 16);
+        const CUtensorMapSwizzle swizzle = dim == 64 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                           : dim == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+        if (encode_rows_map(&maps.kc, K->codes, codes, K->rows, heads_kv, p.row_codes, heads, swizzle) != NVFP4_OK ||
+            encode_rows_map(&maps.vc, V->codes, codes, K->rows, heads_kv, p.row_codes, heads, swizzle) != NVFP4_OK ||
+            encode_rows_map(&maps.ks, K->scales, 16, K->rows, p.row_scales / 16, p.row_scales, groups,
+                            CU_TENSOR_MAP_SWIZZLE_NONE) != NVFP4_OK ||
+            encode_rows_map(&maps.vs, V->scales, 16, K->rows, p.row_scales / 16, p.row_scales, groups,
+                            CU_TENSOR_MAP_SWIZZLE_NONE) != NVFP4_OK)
+            return NVFP4_ERR_CUDA;
+    }
+    return launched(launch_paged_attention(p, maps, (int)dim, static_cast<cudaStream_t>(stream)), 2);
 }
 
 nvfp4_status nvfp4_quantize_swiglu(const void *gate_up, int64_t ld, const nvfp4_tensor *out,

@@ -60,9 +60,9 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kOffset = 6.0f;      // m' is this much below the reference
 constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' moves
 
-constexpr int kWarps = 8;
-constexpr int kStages = 4;
-constexpr int kTile = 16;            // tokens a warp takes at once
+constexpr int kWarps = 8;            // warps that compute; one more brings the tiles in
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kTile = 16;            // tokens of a warp's tile
 
 template <int kD>
 struct Shape {
@@ -70,19 +70,42 @@ struct Shape {
     static constexpr int kScales = kD / 16;
     static constexpr int kChunks = kD / 32;                     // 16-byte pieces of a token's codes
     static constexpr int kSteps = kD / 16;                      // MMA steps over the dims (and M-tiles of O^T)
-    static constexpr int kStage = 2 * kTile * (kCodes + kScales);
-    static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kSum = kWarps * 8 * kD * 4;            // the warps' O, for the join
-    static constexpr int kSmem = kRing + kSum;
     static constexpr int kCtasPerSm = kD == 256 ? 1 : 2;
 };
 
-// Piece of token t where piece `ch` is stored.
+// 16-byte piece `ch` of token t of a tile lies at this piece of the token's
+// row: the swizzle of the copies (64-byte rows: by bits 1 .. 2 of t, 128-byte
+// rows: by bits 0 .. 2, 32-byte rows: none).
 template <int kD>
 __device__ __forceinline__ int swizzled(int ch, int t) {
     if (kD == 64) return ch;
-    if (kD == 128) return ch ^ (t & 2);
-    return ch ^ (2 * (t & 3));
+    if (kD == 128) return ch ^ ((t >> 1) & 3);
+    return ch ^ (t & 7);
+}
+
+// Token of MMA row 2 c + j (rows 8 .. 15: + 8).  Under the swizzle above,
+// the lanes that a shared-memory access serves at once -- two rows' K codes
+// (j = 0, 1), or four tokens' V codes (c = 0 .. 3) -- meet different banks.
+template <int kD>
+__device__ __forceinline__ int token_of(int c, int j) {
+    if (kD == 64) return 4 * j + (c ^ (3 * j));
+    if (kD == 128) return ((c & 1) ^ j) + 2 * j + 4 * (c >> 1);
+    return 2 * (c ^ (2 * j)) + j;
+}
+
+// 3-D tiled TMA load of one box into shared memory, completing on `bar`.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *desc, uint64_t *bar, int32_t x,
+                                            int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        :: "r"(dst), "l"(reinterpret_cast<uint64_t>(desc)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+// Arrives on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -142,19 +165,12 @@ __device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b) {
 }
 
 template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool there) {
-    const int n = there ? kBytes : 0;                           // 0: the destination is zero-filled
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     if (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
     else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" :: "r"(dst), "l"(src), "n"(kBytes), "r"(n) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" :: "n"(kLeft) : "memory");
-}
-
 // __syncwarp as a statement that the reads below cannot move across
 __device__ __forceinline__ void warp_sync() { asm volatile("bar.warp.sync 0xFFFFFFFF;" ::: "memory"); }
 
@@ -197,12 +213,14 @@ __device__ __forceinline__ int tiles_of(int len, int tile_shift) {
 // A position in the list of tiles.
 struct Cursor {
     int b, tile, tiles, len;
-    __device__ __forceinline__ void next(const PagedAttnParams &p, bool more) {
-        if (++tile == tiles) {
+    // n tiles on, n at most to the end of the sequence
+    __device__ __forceinline__ void skip(const PagedAttnParams &p, int n, bool more) {
+        tile += n;
+        if (tile == tiles) {
             ++b;
             tile = 0;
             len = more ? length_of(p, b) : 0;
-            tiles = tiles_of(len, p.tile_shift);
+            tiles = tiles_of(len, p.plan.tile_shift);
         }
     }
 };
@@ -210,28 +228,36 @@ struct Cursor {
 }  // namespace
 
 template <int kD>
-__global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_attention(PagedAttnParams p) {
+__global__ void __launch_bounds__(kThreads, Shape<kD>::kCtasPerSm)
+k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_constant__ PagedMaps maps) {
     using S = Shape<kD>;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ int masks[kWarps][kStages];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
+    __shared__ int masks[kPagedMaxStages][kWarps];
+    __shared__ int rows_sh[kWarps * kTile];              // pool rows of a stage's tokens (copies without TMA)
     __shared__ float ml[kWarps][8][2];
-    __shared__ int64_t warp_sums[kWarps];
+    __shared__ int64_t warp_sums[kWarps + 1];
     __shared__ Cursor start_sh;
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int g = lane >> 2, c = lane & 3;
+    if (tid < p.plan.stages) {
+        mbar_init(&full[tid], p.tma ? 1 : 33);
+        mbar_init(&empty[tid], kWarps);
+    }
+    fence_barrier_init();
+    // what is read from here on may be the result of the kernels before
+    grid_dependency_wait();
 
-    // ---- schedule: this CTA's range [first, first + count) of the tiles
-    int64_t first;
+    // ---- schedule: this CTA's range of the tiles
     int count;
     {
-        const int per = (p.sequences + kWarps * 32 - 1) / (kWarps * 32);
+        const int per = (p.sequences + kThreads - 1) / kThreads;
         const int b0 = min(p.sequences, tid * per), b1 = min(p.sequences, b0 + per);
         int64_t mine = 0;
         for (int b = b0; b < b1; ++b) {
             const int len = p.seq_lens[b];
             if ((len < 0 || len > p.capacity) && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
-            mine += tiles_of(length_of(p, b), p.tile_shift);
+            mine += tiles_of(length_of(p, b), p.plan.tile_shift);
         }
         int64_t upto = mine;
 #pragma unroll
@@ -243,23 +269,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
         __syncthreads();
         int64_t total = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w <= kWarps; ++w) {
             if (w == warp) upto += total;
             total += warp_sums[w];
         }
         const int64_t ranges = min((int64_t)gridDim.x, (total + p.min_tiles - 1) / p.min_tiles);
         const int64_t x = blockIdx.x;
-        first = x < ranges ? x * total / ranges : total;
+        const int64_t first = x < ranges ? x * total / ranges : total;
         const int64_t last = x < ranges ? (x + 1) * total / ranges : total;
         count = (int)(last - first);
         // the threads whose sequences hold the first tile of a range, or
         // start in it, write down what the joining kernel needs
         int64_t at = upto - mine;
         const bool by_sequence = p.sequences <= (int)gridDim.x;
-        if (blockIdx.y == 0 && !by_sequence && tid == 0) p.joins[x] = make_int4(0, 0, 0, 0);
-        if (blockIdx.y == 0 && !by_sequence) __syncthreads();
+        if (blockIdx.y == 0 && !by_sequence) {
+            if (tid == 0) p.joins[x] = make_int4(0, 0, 0, 0);
+            __syncthreads();
+        }
         for (int b = b0; b < b1; ++b) {
-            const int len = length_of(p, b), n = tiles_of(len, p.tile_shift);
+            const int len = length_of(p, b), n = tiles_of(len, p.plan.tile_shift);
             if (at <= first && first < at + n && count > 0) {
                 start_sh.b = b;
                 start_sh.tile = (int)(first - at);
@@ -278,112 +306,238 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
         if (count <= 0) return;
     }
 
-    const int tw_shift = p.tile_shift - 4, tw = 1 << tw_shift;          // warps that share a unit's tokens
-    const int unit_cta = warp >> tw_shift, part = warp & (tw - 1);
-    const int unit = blockIdx.y * p.units_cta + unit_cta;
-    const int hk = unit / p.units_head, head0 = hk * p.group + (unit - hk * p.units_head) * 8;
-    const int heads = min(8, (hk + 1) * p.group - head0);               // query heads of this unit
+    const PagedPlan &plan = p.plan;
+    const int heads_cta = 1 << plan.heads_shift, tw = 1 << plan.parts_shift;
+    const int sub_blocks = plan.units_head >> plan.subs_shift;          // CTAs over the units of a head
+    const int head_first = (int)(blockIdx.y / sub_blocks) << plan.heads_shift;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t v_codes = (uint32_t)(tw * heads_cta * kTile) * S::kCodes;   // within a stage: K codes, V codes, scales
+    const uint32_t k_scales = 2 * v_codes;
+    const int scale_groups = max(1, (heads_cta * S::kScales) >> 4);     // 16-byte groups of a token's scales
+    const uint32_t v_scales = k_scales + tw * scale_groups * (16 * kTile);
+    bool failed = false;
+
+    if (warp == kWarps) {
+        // ================= brings the tiles in =================
+        Cursor at = start_sh;
+        int left = count, stage = 0;
+        uint32_t phase = 1;                                             // of `empty`: the first round passes
+        auto acquire = [&]() {
+            if (!failed && !mbar_wait(&empty[stage], phase, p.timeout)) {
+                failed = true;
+                if (lane == 0) set_status(p.status, ST_TIMEOUT);
+            }
+            failed = __any_sync(0xFFFFFFFFu, failed);
+        };
+        auto advance = [&]() {
+            if (++stage == plan.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        if (p.tma) {
+            // Lane l looks up 16 tokens: part l % tw of tile l / tw of a batch
+            // of tiles of one sequence; the next batch is looked up before
+            // this one is copied.
+            const int per_batch = 32 >> plan.parts_shift, my_part = lane & (tw - 1);
+            struct Batch {
+                int n, page, offset, tokens;
+            };
+            auto lookup = [&]() {
+                Batch f = {0, 0, 0, 0};
+                if (left > 0) {
+                    f.n = min(per_batch, min(left, at.tiles - at.tile));
+                    const int my_tile = lane >> plan.parts_shift;
+                    const int t = ((at.tile + my_tile) << plan.tile_shift) + kTile * my_part;
+                    if (my_tile < f.n && t < at.len) {
+                        const uint32_t entry = quotient((uint32_t)t, p.page_div);
+                        f.offset = t - (int)(entry * p.page_div.d);
+                        f.tokens = min(kTile, at.len - t);
+                        f.page = __ldg(p.block_table + (int64_t)at.b * p.table_stride + entry);
+                    }
+                    left -= f.n;
+                    at.skip(p, f.n, left > 0);
+                }
+                return f;
+            };
+            const int group_first = (head_first * S::kScales) >> 4;
+            const uint32_t bytes = 2u * (heads_cta * kTile * S::kCodes + scale_groups * 16 * kTile);
+            Batch f = lookup();
+            while (f.n > 0) {
+                const Batch next = lookup();
+                if (f.tokens > 0 && (uint32_t)f.page >= (uint32_t)p.n_pages) {
+                    set_status(p.status, ST_INVALID_ARG);
+                    f.tokens = 0;
+                }
+                const int row = f.page * p.page_size + f.offset;
+                for (int i = 0; i < f.n; ++i) {
+                    const int src = (i << plan.parts_shift) + my_part;
+                    const int r = __shfl_sync(0xFFFFFFFFu, row, src);
+                    const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, src);
+                    acquire();
+                    if (failed) break;
+                    const bool mine = lane < tw && tokens > 0;
+                    if (lane < tw) masks[stage][lane] = (1 << tokens) - 1;
+                    const int parts = __popc(__ballot_sync(0xFFFFFFFFu, mine));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], parts * bytes);
+                    __syncwarp();
+                    if (mine) {
+                        const uint32_t to = ring + stage * plan.stage_bytes;
+                        const uint32_t codes = to + lane * (heads_cta * kTile * S::kCodes);
+                        const uint32_t scales = to + lane * (scale_groups * 16 * kTile);
+                        tma_load_3d(codes, &maps.kc, &full[stage], 0, r, head_first);
+                        tma_load_3d(scales + k_scales, &maps.ks, &full[stage], 0, r, group_first);
+                        tma_load_3d(codes + v_codes, &maps.vc, &full[stage], 0, r, head_first);
+                        tma_load_3d(scales + v_scales, &maps.vs, &full[stage], 0, r, group_first);
+                    }
+                    advance();
+                }
+                if (failed) break;
+                f = next;
+            }
+        } else {
+            // Pages that end inside of a tile, or rows that TMA cannot step
+            // by: the rows of a stage's tokens are looked up one stage ahead,
+            // and copied in 16-byte pieces of the codes and kScales of a
+            // head's scales.
+            const int tokens_stage = kTile << plan.parts_shift;
+            const int piece_shift = plan.heads_shift + (kD == 64 ? 1 : kD == 128 ? 2 : 3);
+            const int scales_from = (head_first * S::kScales) & ~15;
+            int pages[4], offsets[4];                                   // tokens lane, lane + 32, ...
+            auto lookup = [&]() {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    pages[k] = -1;
+                    offsets[k] = -1;
+                    const int local = 32 * k + lane, t = (at.tile << plan.tile_shift) + local;
+                    if (left > 0 && local < tokens_stage && t < at.len) {
+                        const uint32_t entry = quotient((uint32_t)t, p.page_div);
+                        offsets[k] = t - (int)(entry * p.page_div.d);
+                        pages[k] = __ldg(p.block_table + (int64_t)at.b * p.table_stride + entry);
+                    }
+                }
+                if (left > 0) at.skip(p, 1, --left > 0);
+            };
+            lookup();
+            for (int i = 0; i < count; ++i) {
+                acquire();
+                if (failed) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    bool ok = offsets[k] >= 0;
+                    if (ok && (uint32_t)pages[k] >= (uint32_t)p.n_pages) {
+                        set_status(p.status, ST_INVALID_ARG);
+                        ok = false;
+                    }
+                    const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
+                    const int local = 32 * k + lane;
+                    if (local < tokens_stage) {
+                        rows_sh[local] = ok ? pages[k] * p.page_size + offsets[k] : -1;
+                        if ((lane & 15) == 0) masks[stage][local >> 4] = (int)((mask >> (lane & 16)) & 0xFFFFu);
+                    }
+                }
+                lookup();
+                __syncwarp();
+                const uint32_t to = ring + stage * plan.stage_bytes;
+                for (int n = lane; n < tokens_stage << piece_shift; n += 32) {
+                    const int t = n >> piece_shift, x = n & ((1 << piece_shift) - 1);
+                    const int h = x / S::kChunks, ch = x % S::kChunks;
+                    const int r = rows_sh[t];
+                    if (r >= 0) {
+                        const int64_t src = (int64_t)r * p.row_codes + (int64_t)(head_first + h) * S::kCodes + 16 * ch;
+                        const uint32_t dst = to + (((t >> 4) << plan.heads_shift) + h) * (kTile * S::kCodes) +
+                                             (t & 15) * S::kCodes + 16 * swizzled<kD>(ch, t & 15);
+                        copy_async<16>(dst, p.kc + src);
+                        copy_async<16>(dst + v_codes, p.vc + src);
+                    }
+                }
+                for (int n = lane; n < tokens_stage << plan.heads_shift; n += 32) {
+                    const int t = n >> plan.heads_shift, h = n & (heads_cta - 1);
+                    const int r = rows_sh[t];
+                    if (r >= 0) {
+                        const int x = (head_first + h) * S::kScales;    // byte of the row
+                        const int64_t src = (int64_t)r * p.row_scales + x;
+                        const uint32_t dst = to + k_scales + ((t >> 4) * scale_groups + ((x - scales_from) >> 4)) * (16 * kTile) +
+                                             (t & 15) * 16 + (x & 15);
+                        copy_async<S::kScales>(dst, p.ks + src);
+                        copy_async<S::kScales>(dst + (v_scales - k_scales), p.vs + src);
+                    }
+                }
+                copies_arrive(&full[stage]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[stage]);               // the masks
+                advance();
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
+        if (failed) {
+            // copies may be under way into stages that nobody waits for
+            for (int n = 0; n < plan.stages; ++n) {
+                mbar_wait(&full[n], 0u, p.timeout);
+                mbar_wait(&full[n], 1u, p.timeout);
+            }
+        }
+        return;
+    }
+
+    // ================= computes =================
+    const int g = lane >> 2, c = lane & 3;
+    const int unit_cta = warp & ((1 << (plan.heads_shift + plan.subs_shift)) - 1);   // unit of this CTA, and part of its tokens
+    const int part = warp >> (plan.heads_shift + plan.subs_shift);
+    const int head_cta = unit_cta >> plan.subs_shift;
+    const int hk = head_first + head_cta;
+    const int sub = (int)((blockIdx.y % sub_blocks) << plan.subs_shift) + (unit_cta & ((1 << plan.subs_shift) - 1));
+    const int unit = hk * plan.units_head + sub;
+    const int head0 = hk * p.group + sub * 8;
+    const int heads = min(8, p.group - sub * 8);                        // query heads of this unit
     const float cscale = __fdiv_rn(__fmul_rn(p.scale, kLog2e), *p.gk);
 
-    const uint32_t ring = smem_u32(smem) + warp * (kStages * S::kStage);
-    const uint8_t *kc = p.kc + hk * S::kCodes, *vc = p.vc + hk * S::kCodes;
-    const uint8_t *ks = p.ks + hk * S::kScales, *vs = p.vs + hk * S::kScales;
-
-    // ---- producer side: the tile at `ahead`; its pages are looked up one
-    // step before its copies are issued
-    Cursor ahead = start_sh;
-    int ahead_left = count;
-    int page = 0, offset = 0;
-    bool there = false;
-    auto lookup = [&]() {
-        there = false;
-        page = offset = 0;
-        if (ahead_left > 0) {
-            const int t = (ahead.tile << p.tile_shift) + part * kTile + (lane & 15);
-            if (t < ahead.len) {
-                const uint32_t entry = quotient((uint32_t)t, p.page_div);
-                offset = t - (int)(entry * p.page_div.d);
-                page = __ldg(p.block_table + (int64_t)ahead.b * p.table_stride + entry);
-                there = true;
-            }
-            --ahead_left;
-            ahead.next(p, ahead_left > 0);
-        }
-    };
-    auto issue = [&](int stage) {
-        bool ok = there;
-        if (ok && (page < 0 || page >= p.n_pages)) {
-            set_status(p.status, ST_INVALID_ARG);
-            ok = false;
-        }
-        const int row = ok ? page * p.page_size + offset : -1;
-        const uint32_t dst = ring + stage * S::kStage;
-        const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok) & 0xFFFFu;
-        if (lane == 0) masks[warp][stage] = (int)mask;
-        if (mask == 0u) return;                                         // no token: nothing will be read
-#pragma unroll
-        for (int i = 0; i < S::kChunks / 2; ++i) {
-            const int n = i * 32 + lane, t = n / S::kChunks, ch = n % S::kChunks;
-            const int r = __shfl_sync(0xFFFFFFFFu, row, t);
-            const int64_t src = r < 0 ? 0 : (int64_t)r * p.row_codes + 16 * ch;
-            const uint32_t to = dst + t * S::kCodes + 16 * swizzled<kD>(ch, t);
-            copy_async<16>(to, kc + src, r >= 0);
-            copy_async<16>(to + kTile * S::kCodes, vc + src, r >= 0);
-        }
-        {   // lanes 0 .. 15: K scales of token `lane`; 16 .. 31: V scales
-            const int64_t src = row < 0 ? 0 : (int64_t)row * p.row_scales;
-            copy_async<S::kScales>(dst + 2 * kTile * S::kCodes + lane * S::kScales,
-                                   (lane < 16 ? ks : vs) + src, row >= 0);
-        }
-    };
-    lookup();
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        issue(s);
-        copies_commit();
-        lookup();
-    }
-
-    // ---- lane constants of the fragment reads
-    const int tk = 4 * (g & 1) + ((g >> 1) ^ (3 * (g & 1)));            // token of MMA row g (row g + 8: + 8)
-    const int ta = c, tb = 4 + (c ^ 3);                                 // tokens of MMA rows 2c, 2c + 1
+    // ---- lane constants of the fragment reads, from the start of a stage
+    const int tk = token_of<kD>(g >> 1, g & 1);                         // token of MMA row g (row g + 8: + 8)
+    const int ta = token_of<kD>(c, 0), tb = token_of<kD>(c, 1);         // tokens of MMA rows 2c, 2c + 1
     constexpr int kVWords = kD / 64;                                    // words of V codes a lane takes per token
     constexpr int kKWords = kD == 64 ? 2 : 4;
-    uint32_t k_at[2], va_at, vb_at;
-    if (kD == 64) {
-        k_at[0] = k_at[1] = tk * S::kCodes + 8 * c;
-        va_at = ta * S::kCodes + 4 * g;
-        vb_at = tb * S::kCodes + 4 * g;
-    } else if (kD == 128) {
-        k_at[0] = k_at[1] = tk * S::kCodes + 16 * swizzled<kD>(c, tk);
-        va_at = ta * S::kCodes + 16 * swizzled<kD>(g >> 1, ta) + 8 * (g & 1);
-        vb_at = tb * S::kCodes + 16 * swizzled<kD>(g >> 1, tb) + 8 * (g & 1);
-    } else {
-        k_at[0] = tk * S::kCodes + 16 * swizzled<kD>(c, tk);
-        k_at[1] = tk * S::kCodes + 16 * swizzled<kD>(c + 4, tk);
-        va_at = ta * S::kCodes + 16 * swizzled<kD>(g, ta);
-        vb_at = tb * S::kCodes + 16 * swizzled<kD>(g, tb);
+    uint32_t k_at[2], va_at, vb_at, ks_at, vs_at;
+    {
+        const uint32_t tile = ((part << plan.heads_shift) + head_cta) * (kTile * S::kCodes);
+        if (kD == 64) {
+            k_at[0] = k_at[1] = tile + tk * S::kCodes + 8 * c;
+            va_at = ta * S::kCodes + 4 * g;
+            vb_at = tb * S::kCodes + 4 * g;
+        } else if (kD == 128) {
+            k_at[0] = k_at[1] = tile + tk * S::kCodes + 16 * swizzled<kD>(c, tk);
+            va_at = ta * S::kCodes + 16 * swizzled<kD>(g >> 1, ta) + 8 * (g & 1);
+            vb_at = tb * S::kCodes + 16 * swizzled<kD>(g >> 1, tb) + 8 * (g & 1);
+        } else {
+            k_at[0] = tile + tk * S::kCodes + 16 * swizzled<kD>(c, tk);
+            k_at[1] = tile + tk * S::kCodes + 16 * swizzled<kD>(c + 4, tk);
+            va_at = ta * S::kCodes + 16 * swizzled<kD>(g, ta);
+            vb_at = tb * S::kCodes + 16 * swizzled<kD>(g, tb);
+        }
+        va_at += tile + v_codes;
+        vb_at += tile + v_codes;
+        const int x = hk * S::kScales;
+        const uint32_t scales = (part * scale_groups + ((x - ((head_first * S::kScales) & ~15)) >> 4)) * (16 * kTile) + (x & 15);
+        ks_at = k_scales + scales + tk * 16 + (kD == 64 ? c : 2 * c);
+        vs_at = v_scales + scales + (kD == 64 ? g >> 1 : kD == 128 ? g : 2 * g);
     }
-    va_at += kTile * S::kCodes;
-    vb_at += kTile * S::kCodes;
-    constexpr uint32_t kScaleAt = 2 * kTile * S::kCodes;
-    const uint32_t ks_at = kScaleAt + tk * S::kScales + (kD == 64 ? c : 2 * c);
-    const uint32_t vs_at = kScaleAt + kTile * S::kScales + (kD == 64 ? g >> 1 : kD == 128 ? g : 2 * g);
 
-    // ---- consumer side
-    Cursor now = start_sh;
     uint32_t qb[2 * S::kSteps];          // B fragments of the query
     float oacc[S::kSteps][4];
-    float lsum[2] = {0.0f, 0.0f}, mp[2] = {kLowest, kLowest}, ck[2] = {0.0f, 0.0f};
-    bool fresh = true, starts_here = now.tile == 0;
+    float lsum[2], mp[2], ck[2];
+    int b = start_sh.b, in_seq = start_sh.tiles - start_sh.tile;        // tiles to the end of the sequence
+    bool starts_here = start_sh.tile == 0;
+    int left = count, stage = 0;
+    uint32_t phase = 0, at = ring;
+    // the warps' O, where several share a unit's tokens
+    float *sums = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
 
-    for (int i = 0; i < count; ++i) {
-        if (fresh) {
-            fresh = false;
-            // query of head g: lane c holds dims kD / 4 * c ... (kD = 256: 32c .. + 31 and 128 + 32c .. + 31)
+    while (true) {
+        {   // query of head g: lane c holds dims kD / 4 * c ... (kD = 256: 32c .. + 31 and 128 + 32c .. + 31)
             uint4 w[kD / 32];
             uint32_t amax = 0u;
-            const uint16_t *q = p.q + (int64_t)now.b * p.qs_b + (int64_t)(head0 + g) * p.qs_h;
+            const uint16_t *q = p.q + (int64_t)b * p.qs_b + (int64_t)(head0 + g) * p.qs_h;
 #pragma unroll
             for (int n = 0; n < kD / 32; ++n) {
                 const int d = kD == 256 ? 32 * c + 8 * (n & 3) + 128 * (n >> 2) : (kD / 4) * c + 8 * n;
@@ -398,7 +552,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
             // zeros, infinities or NaN stays as it is
             const int up = e == 0u || e == 255u ? 0 : min(141 - (int)e, 126);
             const float mult = __uint_as_float((uint32_t)(127 + up) << 23);
-            const float undo = __uint_as_float(up > 126 ? 0u : (uint32_t)(127 - up) << 23);
+            const float undo = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll
             for (int n = 0; n < kD / 32; ++n) {
                 const uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
@@ -417,31 +571,34 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
 #pragma unroll
                 for (int n = 0; n < 4; ++n) oacc[j][n] = 0.0f;
         }
-        const int stage = i % kStages;
-        copies_wait<kStages - 2>();
-        warp_sync();
-        issue((i + kStages - 1) % kStages);
-        copies_commit();
-        lookup();
-        const uint32_t at = ring + stage * S::kStage;
-        const uint32_t mask = (uint32_t)masks[warp][stage];
-
-        if (mask != 0u) {
+        const bool ends = in_seq <= left;                               // the sequence ends in this range
+        const int n_tiles = ends ? in_seq : left;
+        left -= n_tiles;
+        for (int tile = n_tiles; tile > 0; --tile) {
+            // A wait that gives up leaves the CTA in step: its tiles then
+            // count as empty, every barrier is still met.
+            if (!failed && !mbar_wait(&full[stage], phase, p.timeout)) {
+                failed = true;
+                set_status(p.status, ST_TIMEOUT);
+            }
+            failed = __any_sync(0xFFFFFFFFu, failed);
+            const uint32_t mask = failed ? 0u : (uint32_t)masks[stage][part];
+            if (mask != 0u) {
             // ---- S = K q^T
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int half = 0; half < (kD == 256 ? 2 : 1); ++half) {
+            for (int part_k = 0; part_k < (kD == 256 ? 2 : 1); ++part_k) {
                 uint32_t w0[kKWords], w1[kKWords];
-                lds_words<kKWords>(at + k_at[half], w0);
-                lds_words<kKWords>(at + k_at[half] + 8 * S::kCodes, w1);
+                lds_words<kKWords>(at + k_at[part_k], w0);
+                lds_words<kKWords>(at + k_at[part_k] + 8 * S::kCodes, w1);
                 uint32_t s0[2], s1[2];                                  // scales of rows g, g + 8 as (s, s)
                 if (kD == 64) {
-                    const uint32_t x = f16x2_from_e4m3x2(lds8(at + ks_at) | (lds8(at + ks_at + 8 * S::kScales) << 8));
+                    const uint32_t x = f16x2_from_e4m3x2(lds8(at + ks_at) | (lds8(at + ks_at + 128) << 8));
                     s0[0] = s0[1] = __byte_perm(x, x, 0x1010);
                     s1[0] = s1[1] = __byte_perm(x, x, 0x3232);
                 } else {
-                    const uint32_t x0 = f16x2_from_e4m3x2(lds16(at + ks_at + 8 * half));
-                    const uint32_t x1 = f16x2_from_e4m3x2(lds16(at + ks_at + 8 * half + 8 * S::kScales));
+                    const uint32_t x0 = f16x2_from_e4m3x2(lds16(at + ks_at + 8 * part_k));
+                    const uint32_t x1 = f16x2_from_e4m3x2(lds16(at + ks_at + 8 * part_k + 128));
                     s0[0] = __byte_perm(x0, x0, 0x1010);
                     s0[1] = __byte_perm(x0, x0, 0x3232);
                     s1[0] = __byte_perm(x1, x1, 0x1010);
@@ -449,18 +606,18 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
                 }
 #pragma unroll
                 for (int n = 0; n < kKWords; ++n) {                     // two MMA steps a word
-                    uint32_t a[4], b[4];
-                    f16x2_from_word(w0[n], a);
-                    f16x2_from_word(w1[n], b);
+                    uint32_t x[4], y[4];
+                    f16x2_from_word(w0[n], x);
+                    f16x2_from_word(w1[n], y);
                     const int blk = n / 2;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        a[k] = mul_f16x2(a[k], s0[blk]);
-                        b[k] = mul_f16x2(b[k], s1[blk]);
+                        x[k] = mul_f16x2(x[k], s0[blk]);
+                        y[k] = mul_f16x2(y[k], s1[blk]);
                     }
-                    const int step = 8 * half + 2 * n;
-                    mma_f16(s, a[0], b[0], a[1], b[1], qb[2 * step], qb[2 * step + 1]);
-                    mma_f16(s, a[2], b[2], a[3], b[3], qb[2 * step + 2], qb[2 * step + 3]);
+                    const int step = 8 * part_k + 2 * n;
+                    mma_f16(s, x[0], y[0], x[1], y[1], qb[2 * step], qb[2 * step + 1]);
+                    mma_f16(s, x[2], y[2], x[3], y[3], qb[2 * step + 2], qb[2 * step + 3]);
                 }
             }
             // ---- weights: e = S c - m', rows tk and tk + 8, heads 2c and 2c + 1
@@ -493,13 +650,12 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
                     if (r1) e[n + 2] = __fmaf_rn(s[n + 2], ck[n], -mn);
                 }
             }
-            float w[4];
 #pragma unroll
-            for (int n = 0; n < 4; ++n) w[n] = exp2_fast(e[n]);
-            lsum[0] += w[0] + w[2];
-            lsum[1] += w[1] + w[3];
-            const uint32_t p0 = transpose_8x8(f16x2_from_f32(w[0], w[1]));
-            const uint32_t p1 = transpose_8x8(f16x2_from_f32(w[2], w[3]));
+            for (int n = 0; n < 4; ++n) e[n] = exp2_fast(e[n]);
+            lsum[0] += e[0] + e[2];
+            lsum[1] += e[1] + e[3];
+            const uint32_t p0 = transpose_8x8(f16x2_from_f32(e[0], e[1]));
+            const uint32_t p1 = transpose_8x8(f16x2_from_f32(e[2], e[3]));
 
             // ---- O^T += V^T P^T
             uint32_t wa[2][kVWords], wb[2][kVWords], sc[2][2];          // [rows 2c.. / 2c + 8 ..]
@@ -508,14 +664,25 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
                 lds_words<kVWords>(at + va_at + 8 * n * S::kCodes, wa[n]);
                 lds_words<kVWords>(at + vb_at + 8 * n * S::kCodes, wb[n]);
                 if (kD == 256) {
-                    const uint32_t a = lds16(at + vs_at + (ta + 8 * n) * S::kScales);
-                    const uint32_t b = lds16(at + vs_at + (tb + 8 * n) * S::kScales);
-                    sc[n][0] = f16x2_from_e4m3x2(__byte_perm(a, b, 0x0040));
-                    sc[n][1] = f16x2_from_e4m3x2(__byte_perm(a, b, 0x0051));
+                    const uint32_t x = lds16(at + vs_at + (ta + 8 * n) * 16);
+                    const uint32_t y = lds16(at + vs_at + (tb + 8 * n) * 16);
+                    sc[n][0] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0040));
+                    sc[n][1] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0051));
                 } else {
-                    const uint32_t a = lds8(at + vs_at + (ta + 8 * n) * S::kScales);
-                    const uint32_t b = lds8(at + vs_at + (tb + 8 * n) * S::kScales);
-                    sc[n][0] = sc[n][1] = f16x2_from_e4m3x2(a | (b << 8));
+                    const uint32_t x = lds8(at + vs_at + (ta + 8 * n) * 16);
+                    const uint32_t y = lds8(at + vs_at + (tb + 8 * n) * 16);
+                    sc[n][0] = sc[n][1] = f16x2_from_e4m3x2(x | (y << 8));
+                }
+            }
+            if (mask != 0xFFFFu) {
+                // what lies in the rows of absent tokens is not theirs: with
+                // a scale of 0 their values count 0 (any code is finite)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const uint32_t keep = (((mask >> (ta + 8 * n)) & 1u) ? 0xFFFFu : 0u) |
+                                          (((mask >> (tb + 8 * n)) & 1u) ? 0xFFFF0000u : 0u);
+                    sc[n][0] &= keep;
+                    sc[n][1] &= keep;
                 }
             }
 #pragma unroll
@@ -525,7 +692,7 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
                 for (int h = 0; h < 2; ++h) {
                     f16x2_from_word(nibbles(wa[h][n], wb[h][n] << 4), even[h]);
                     f16x2_from_word(nibbles(wa[h][n] >> 4, wb[h][n]), odd[h]);
-                    const uint32_t x = sc[h][n / 2 < 2 ? (kD == 256 ? n / 2 : 0) : 0];
+                    const uint32_t x = sc[h][kD == 256 ? n / 2 : 0];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         even[h][k] = mul_f16x2(even[h][k], x);
@@ -535,177 +702,188 @@ __global__ void __launch_bounds__(kWarps * 32, Shape<kD>::kCtasPerSm) k_paged_at
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_f16(oacc[4 * n + k], even[0][k], odd[0][k], even[1][k], odd[1][k], p0, p1);
             }
+            }
+            warp_sync();
+            if (lane == 0) mbar_arrive(&empty[stage]);
+            at += plan.stage_bytes;
+            if (++stage == plan.stages) {
+                stage = 0;
+                phase ^= 1u;
+                at = ring;
+            }
         }
 
-        // ---- end of this CTA's part of a sequence
-        const bool ends = now.tile + 1 == now.tiles;
-        if (ends || i + 1 == count) {
+        // ---- end of this CTA's part of the sequence: join the unit's warps
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int off = 4; off <= 16; off <<= 1) lsum[n] += __shfl_xor_sync(0xFFFFFFFFu, lsum[n], off);
-            float M[2] = {mp[0], mp[1]}, L[2] = {lsum[0], lsum[1]};
-            if (tw > 1) {
-                if (g == 0) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        ml[warp][2 * c + n][0] = mp[n];
-                        ml[warp][2 * c + n][1] = lsum[n];
-                    }
-                }
-                unit_barrier(1 + unit_cta, 32 * tw);
-                const int w0 = warp - part;
+            for (int off = 4; off <= 16; off <<= 1) lsum[n] += __shfl_xor_sync(0xFFFFFFFFu, lsum[n], off);
+        float M[2] = {mp[0], mp[1]}, L[2] = {lsum[0], lsum[1]};
+        if (tw > 1) {
+            if (g == 0) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    for (int w = 0; w < tw; ++w) M[n] = fmaxf(M[n], ml[w0 + w][2 * c + n][0]);
-                    L[n] = 0.0f;
-                    for (int w = 0; w < tw; ++w) L[n] += ml[w0 + w][2 * c + n][1] * exp2_fast(ml[w0 + w][2 * c + n][0] - M[n]);
-                }
-                const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
-                float *mine = reinterpret_cast<float *>(smem + S::kRing) + warp * (8 * kD) + lane;
-#pragma unroll
-                for (int j = 0; j < S::kSteps; ++j)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
-                unit_barrier(1 + unit_cta, 32 * tw);
-            }
-            const bool whole = ends && starts_here;
-            const float *from = reinterpret_cast<const float *>(smem + S::kRing) + (warp - part) * (8 * kD) + lane;
-            const int64_t slot = ((int64_t)(2 * blockIdx.x + (starts_here ? 1 : 0)) * gridDim.y + blockIdx.y) * p.units_cta + unit_cta;
-            float *part_o = p.part_o + slot * (8 * kD) + lane;
-            const float inv_gv = *p.gv;
-#pragma unroll
-            for (int j = 0; j < S::kSteps; ++j) {
-                if ((j & (tw - 1)) != part) continue;
-                float r[4];
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    r[n] = oacc[j][n];
-                    if (tw > 1) {
-                        r[n] = 0.0f;
-                        for (int w = 0; w < tw; ++w) r[n] += from[w * (8 * kD) + (4 * j + n) * 32];
-                    }
-                }
-                if (whole) {
-#pragma unroll
-                    for (int n = 0; n < 2; ++n) {
-                        if (2 * c + n < heads) {
-                            const bool none = L[n] == 0.0f;
-                            const float lo = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n], L[n]), inv_gv);
-                            const float hi = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n + 2], L[n]), inv_gv);
-                            *reinterpret_cast<uint32_t *>(p.o + (int64_t)now.b * p.os_b + (int64_t)(head0 + 2 * c + n) * p.os_h +
-                                                          (kD / 8) * g + 2 * j) = bf16x2_from_f32(lo, hi);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) part_o[(4 * j + n) * 32] = r[n];
+                    ml[warp][2 * c + n][0] = mp[n];
+                    ml[warp][2 * c + n][1] = lsum[n];
                 }
             }
-            if (part == 0 && g == 0) {
+            unit_barrier(1 + unit_cta, 32 * tw);
+            const int w0 = unit_cta, step = kWarps >> plan.parts_shift;
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    if (whole) {
-                        if (p.lse != nullptr && 2 * c + n < heads)
-                            p.lse[(int64_t)now.b * p.heads_q + head0 + 2 * c + n] =
-                                L[n] == 0.0f ? -__int_as_float(0x7F800000) : (M[n] + log2f(L[n])) * kLn2;
-                    } else {
-                        p.part_ml[slot * 8 + 2 * c + n] = make_float2(M[n], L[n]);
-                    }
-                }
+            for (int n = 0; n < 2; ++n) {
+                for (int w = 0; w < tw; ++w) M[n] = fmaxf(M[n], ml[w0 + w * step][2 * c + n][0]);
+                L[n] = 0.0f;
+                for (int w = 0; w < tw; ++w) L[n] += ml[w0 + w * step][2 * c + n][1] * exp2_fast(ml[w0 + w * step][2 * c + n][0] - M[n]);
             }
-            fresh = true;
-            starts_here = true;
+            const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
+            float *mine = sums + warp * (8 * kD) + lane;
+#pragma unroll
+            for (int j = 0; j < S::kSteps; ++j)
+#pragma unroll
+                for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
+            unit_barrier(1 + unit_cta, 32 * tw);
         }
-        now.next(p, i + 1 < count);
+        const bool whole = ends && starts_here;
+        const float *from = sums + unit_cta * (8 * kD) + lane;
+        const int64_t slot = (int64_t)(2 * blockIdx.x + (starts_here ? 1 : 0)) * plan.units + unit;
+        float *part_o = p.part_o + slot * (8 * kD) + lane;
+        const float gv = *p.gv;
+#pragma unroll
+        for (int j = 0; j < S::kSteps; ++j) {
+            if ((j & (tw - 1)) != part) continue;
+            float r[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                r[n] = oacc[j][n];
+                if (tw > 1) {
+                    r[n] = 0.0f;
+                    for (int w = 0; w < tw; ++w) r[n] += from[w * (kWarps >> plan.parts_shift) * (8 * kD) + (4 * j + n) * 32];
+                }
+            }
+            if (whole) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (2 * c + n < heads) {
+                        const bool none = L[n] == 0.0f;
+                        const float lo = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n], L[n]), gv);
+                        const float hi = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n + 2], L[n]), gv);
+                        *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + 2 * c + n) * p.os_h +
+                                                      (kD / 8) * g + 2 * j) = bf16x2_from_f32(lo, hi);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < 4; ++n) part_o[(4 * j + n) * 32] = r[n];
+            }
+        }
+        if (part == 0 && g == 0) {
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (whole) {
+                    if (p.lse != nullptr && 2 * c + n < heads)
+                        p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] =
+                            L[n] == 0.0f ? -__int_as_float(0x7F800000) : (M[n] + log2f(L[n])) * kLn2;
+                } else {
+                    p.part_ml[slot * 8 + 2 * c + n] = make_float2(M[n], L[n]);
+                }
+            }
+        }
+        if (left == 0) break;
+        ++b;
+        in_seq = tiles_of(length_of(p, b), plan.tile_shift);
+        starts_here = true;
     }
 }
 
-// Joins the parts of the sequences that were cut: one sequence (or the one
-// that is cut at the end of a range) per blockIdx.x, M-tiles of O^T (128
-// values) in turn per blockIdx.y.  The parts of a tile are dealt to 8 groups
-// of 32 threads, whose sums are added in order.
-__global__ void __launch_bounds__(256) k_paged_combine(PagedAttnParams p, int dim, int ranges_x, int blocks_y) {
-    __shared__ float weight[kPagedMaxRanges][8];
-    __shared__ float red[32][8];
+// Joins the parts of the sequences that were cut: blockIdx.x is the sequence
+// (or the range at whose end one is cut), blockIdx.y takes M-tiles of O^T (128
+// values of a unit).  Eight warps take the parts in turn, four at a time, each
+// with the running maximum and sum of the online softmax, and are joined in
+// shared memory; a part's maxima, sums and values are one round of loads.
+__global__ void __launch_bounds__(256) k_paged_combine(const __grid_constant__ PagedAttnParams p, int dim) {
+    __shared__ float2 ml[8][8];
     __shared__ float4 sums[8][32];
-    __shared__ float M_sh[8], L_sh[8];
     grid_dependency_wait();
     const int4 join = p.joins[blockIdx.x];
     const int b = join.x, x0 = join.y, pieces = join.z;
     if (pieces <= 1) return;
-    const int tid = threadIdx.x, tiles = dim / 16, units = blocks_y * p.units_cta;
-    const int total = units * tiles;
-    int done = -1;
-    for (int item = blockIdx.y; item < total; item += gridDim.y) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tiles = dim / 16, units = p.plan.units;
+    // values 4 lane .. + 3 of an M-tile: [n = 0 .. 3][lane of the MMA]; four
+    // neighbouring lanes are heads 0, 2, 4, 6 (n even) or 1, 3, 5, 7 (n odd)
+    const int odd = (lane >> 3) & 1;
+    for (int item = blockIdx.y; item < units * tiles; item += gridDim.y) {
         const int unit = item / tiles, j = item - unit * tiles;
-        const int hk = unit / p.units_head, head0 = hk * p.group + (unit - hk * p.units_head) * 8;
-        const int heads = min(8, (hk + 1) * p.group - head0);
-        // piece n: the first lies in the second slot of its CTA, the others in the first
-        auto slot = [&](int n) { return (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit; };
-        if (unit != done) {
-            done = unit;
-            const int h = tid & 7, group = tid >> 3;
-            float m = kLowest;
-            for (int n = group; n < pieces; n += 32) m = fmaxf(m, p.part_ml[slot(n) * 8 + h].x);
-            __syncthreads();
-            red[group][h] = m;
-            __syncthreads();
-            if (tid < 8) {
-                for (int n = 1; n < 32; ++n) m = fmaxf(m, red[n][tid]);
-                M_sh[tid] = m;
-            }
-            __syncthreads();
-            m = M_sh[h];
-            float l = 0.0f;
-            for (int n = group; n < pieces; n += 32) {
-                const float2 v = p.part_ml[slot(n) * 8 + h];
-                const float w = exp2_fast(v.x - m);
-                weight[n][h] = w;
-                l += w * v.y;
-            }
-            red[group][h] = l;
-            __syncthreads();
-            if (tid < 8) {
-                l = 0.0f;
-                for (int n = 0; n < 32; ++n) l += red[n][tid];
-                L_sh[tid] = l;
-                if (j == 0 && p.lse != nullptr && tid < heads)
-                    p.lse[(int64_t)b * p.heads_q + head0 + tid] =
-                        l == 0.0f ? -__int_as_float(0x7F800000) : (M_sh[tid] + log2f(l)) * kLn2;
-            }
-            __syncthreads();
-        }
-        // 128 values: [n = 0 .. 3][lane], four neighbouring lanes (c = 0 .. 3)
-        // a thread: heads 0, 2, 4, 6 (n even) or 1, 3, 5, 7 (n odd)
-        const int v = tid & 31, group = tid >> 5, n4 = v >> 3, odd = n4 & 1;
+        float m = kLowest, l = 0.0f;                                     // of head lane % 8
         float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int n = group; n < pieces; n += 8) {
-            const float4 o = *reinterpret_cast<const float4 *>(p.part_o + slot(n) * (8 * dim) + 128 * j + 4 * v);
-            a.x += o.x * weight[n][odd];
-            a.y += o.y * weight[n][2 + odd];
-            a.z += o.z * weight[n][4 + odd];
-            a.w += o.w * weight[n][6 + odd];
+        for (int n0 = 4 * warp; n0 < pieces; n0 += 32) {
+            // piece n: the first lies in the second slot of its range, the others in the first
+            float4 o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = min(n0 + k, pieces - 1);
+                const int64_t slot = (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit;
+                o[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot * (8 * dim) + 128 * j) + lane);
+            }
+            const int n = n0 + (lane >> 3);
+            float2 v = make_float2(kLowest, 0.0f);
+            if (n < pieces) {
+                const int64_t slot = (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit;
+                v = __ldcg(p.part_ml + slot * 8 + (lane & 7));
+            }
+            float top = fmaxf(m, v.x);
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+            const float alpha = exp2_fast(m - top), w = n < pieces ? exp2_fast(v.x - top) : 0.0f;
+            m = top;
+            float wl = w * v.y;
+            wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 8);
+            wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 16);
+            l = l * alpha + wl;
+            a.x *= __shfl_sync(0xFFFFFFFFu, alpha, odd);
+            a.y *= __shfl_sync(0xFFFFFFFFu, alpha, 2 + odd);
+            a.z *= __shfl_sync(0xFFFFFFFFu, alpha, 4 + odd);
+            a.w *= __shfl_sync(0xFFFFFFFFu, alpha, 6 + odd);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w0 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + odd), w1 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 2 + odd);
+                const float w2 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 4 + odd), w3 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 6 + odd);
+                if (n0 + k < pieces) {
+                    a.x += o[k].x * w0;
+                    a.y += o[k].y * w1;
+                    a.z += o[k].z * w2;
+                    a.w += o[k].w * w3;
+                }
+            }
         }
-        sums[group][v] = a;
+        sums[warp][lane] = a;
+        if (lane < 8) ml[warp][lane] = make_float2(m, l);
         __syncthreads();
+        const int tid = threadIdx.x;
         if (tid < 64) {
             // one head and lane row g: values n = e and n = e + 2 (dims 2j, 2j + 1)
-            const int h = tid & 7, gg = tid >> 3, e = h & 1, cc = h >> 1;
-            const float *f = reinterpret_cast<const float *>(&sums[0][0]);
-            float lo = 0.0f, hi = 0.0f;
+            const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
+            const int head0 = hk * p.group + sub * 8, heads = min(8, p.group - sub * 8);
+            const int h = tid & 7, g = tid >> 3, e = h & 1, c = h >> 1;
+            const float *f = reinterpret_cast<const float *>(&sums[0][0]) + g * 4 + c;
+            float M = kLowest, L = 0.0f, lo = 0.0f, hi = 0.0f;
+#pragma unroll
+            for (int n = 0; n < 8; ++n) M = fmaxf(M, ml[n][h].x);
 #pragma unroll
             for (int n = 0; n < 8; ++n) {
-                lo += f[n * 128 + e * 32 + gg * 4 + cc];
-                hi += f[n * 128 + (e + 2) * 32 + gg * 4 + cc];
+                const float w = exp2_fast(ml[n][h].x - M);
+                L += w * ml[n][h].y;
+                lo += w * f[n * 128 + e * 32];
+                hi += w * f[n * 128 + (e + 2) * 32];
             }
             if (h < heads) {
-                const float L = L_sh[h], gv = *p.gv;
+                const float gv = *p.gv;
                 lo = L == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(lo, L), gv);
                 hi = L == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(hi, L), gv);
                 *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + h) * p.os_h +
-                                              (dim / 8) * gg + 2 * j) = bf16x2_from_f32(lo, hi);
+                                              (dim / 8) * g + 2 * j) = bf16x2_from_f32(lo, hi);
+                if (j == 0 && g == 0 && p.lse != nullptr)
+                    p.lse[(int64_t)b * p.heads_q + head0 + h] = L == 0.0f ? -__int_as_float(0x7F800000) : (M + log2f(L)) * kLn2;
             }
         }
         __syncthreads();
@@ -714,43 +892,52 @@ __global__ void __launch_bounds__(256) k_paged_combine(PagedAttnParams p, int di
 
 namespace {
 
-template <int kD>
-cudaError_t launch_main(const PagedAttnParams &p, dim3 grid, cudaStream_t s) {
-    static std::atomic<uint64_t> ready{0};               // devices (below 64) with the shared memory allowed
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (!((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
-        e = cudaFuncSetAttribute(k_paged_attention<kD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kD>::kSmem);
-        if (e != cudaSuccess) return e;
-        ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
-    k_paged_attention<kD><<<grid, kWarps * 32, Shape<kD>::kSmem, s>>>(p);
-    return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_paged_attention(const PagedAttnParams &p, int dim, const PagedPlan &plan, cudaStream_t s) {
-    const dim3 grid((unsigned)plan.ranges, (unsigned)plan.blocks);
-    cudaError_t e = dim == 64 ? launch_main<64>(p, grid, s)
-                    : dim == 128 ? launch_main<128>(p, grid, s)
-                                 : launch_main<256>(p, grid, s);
-    if (e != cudaSuccess) return e;
-    // the sequences that can be cut, and CTAs for about one wave of the device
-    const int joins = std::min(p.sequences, plan.ranges);
-    const int tiles = plan.blocks * p.units_cta * (dim / 16);
-    const int per = std::max(1, (int)(((int64_t)joins * tiles + 1183) / 1184));
+cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t smem, cudaStream_t s, void **args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)joins, (unsigned)((tiles + per - 1) / per));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_paged_combine, p, dim, plan.ranges, plan.blocks);
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+template <int kD>
+cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
+    static std::atomic<uint64_t> ready{0};               // devices (below 64) with the shared memory allowed
+    const void *kernel = (const void *)k_paged_attention<kD>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!((ready.load(std::memory_order_relaxed) >> dev) & 1u)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kD == 256 ? kPagedSmem256 : kPagedSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    void *args[] = {const_cast<PagedAttnParams *>(&p), const_cast<PagedMaps *>(&maps)};
+    return launch_dependent(kernel, dim3((unsigned)p.plan.ranges, (unsigned)p.plan.blocks), kThreads,
+                            (size_t)p.plan.smem, s, args);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_attention(const PagedAttnParams &p, const PagedMaps &maps, int dim, cudaStream_t s) {
+    cudaError_t e = dim == 64 ? launch_main<64>(p, maps, s)
+                    : dim == 128 ? launch_main<128>(p, maps, s)
+                                 : launch_main<256>(p, maps, s);
+    if (e != cudaSuccess) return e;
+    // the sequences that can be cut, and CTAs for about one wave of the device
+    const int joins = std::min(p.sequences, p.plan.ranges);
+    const int tiles = p.plan.units * (dim / 16);
+    const int per = std::max(1, (int)(((int64_t)joins * tiles + 1183) / 1184));
+    void *args[] = {const_cast<PagedAttnParams *>(&p), &dim};
+    return launch_dependent((const void *)k_paged_combine, dim3((unsigned)joins, (unsigned)((tiles + per - 1) / per)),
+                            256, 0, s, args);
 }
 
 }  // namespace nvfp4

@@ -273,30 +273,56 @@ __global__ void k_kv_read(KvReadParams p);
 // Decode attention over a paged cache (attention_paged.cu).
 //
 // The launch plan, by the head counts alone (so that the scratch does not
-// depend on lengths or device): units (a KV head with up to 8 query heads),
-// units a CTA takes, CTAs over the units and ranges of the tile list.
+// depend on lengths or device).  A unit is a KV head with up to 8 of its query
+// heads.  The 8 computing warps of a CTA are heads_cta x subs x parts (powers
+// of two): neighbouring KV heads, units of one head, and 16-token parts of
+// the tile of 16 x parts tokens that a stage of the ring holds.
 constexpr int kPagedMaxRanges = 296;
+constexpr int kPagedMaxStages = 8;
 constexpr int kPagedMinTiles = 1;
+constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
+constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
+#ifndef PU
+#define PU 8
+#endif
 struct PagedPlan {
-    int units_head;          // units of a KV head
-    int units_cta, tile_shift, blocks, ranges;
+    int units_head, units;                   // units of a KV head, of all
+    int heads_shift, subs_shift, parts_shift, tile_shift;
+    int blocks, ranges;                      // CTAs over the units; ranges of the tile list
+    int stages, stage_bytes, smem;
 };
 inline PagedPlan paged_plan(int heads_q, int heads_kv, int dim) {
     PagedPlan n;
     n.units_head = (heads_q / heads_kv + 7) / 8;
-    const int units = heads_kv * n.units_head;
-    n.units_cta = units % 4 == 0 ? 4 : units % 2 == 0 ? 2 : 1;
-    n.tile_shift = n.units_cta == 4 ? 5 : n.units_cta == 2 ? 6 : 7;   // 16 tokens x 8 / units_cta warps
-    n.blocks = units / n.units_cta;
+    n.units = heads_kv * n.units_head;
+    n.subs_shift = n.units_head % 4 == 0 ? 2 : n.units_head % 2 == 0 ? 1 : 0;
+    n.heads_shift = 0;
+    while ((2 << (n.heads_shift + n.subs_shift)) <= PU && heads_kv % (2 << n.heads_shift) == 0) ++n.heads_shift;
+    n.parts_shift = 3 - n.subs_shift - n.heads_shift;
+    n.tile_shift = 4 + n.parts_shift;
+    n.blocks = (heads_kv >> n.heads_shift) * (n.units_head >> n.subs_shift);
     const int ctas = dim == 256 ? 148 : 296;                          // one wave of 148 SMs
     n.ranges = ctas / n.blocks > 1 ? ctas / n.blocks : 1;
+    const int heads = 1 << n.heads_shift, parts = 1 << n.parts_shift;
+    const int groups = heads * (dim / 16) / 16 > 1 ? heads * (dim / 16) / 16 : 1;
+    n.stage_bytes = (2 * parts * 16 * (heads * (dim / 2) + groups * 16) + 1023) / 1024 * 1024;
+    const int sums = parts > 1 ? 8 * 8 * dim * 4 : 0;                  // the warps' O
+    const int room = (dim == 256 ? kPagedSmem256 : kPagedSmem) - 1024 - sums;
+    n.stages = room / n.stage_bytes < kPagedMaxStages ? room / n.stage_bytes : kPagedMaxStages;
+    n.smem = 1024 + n.stages * n.stage_bytes + sums;
     return n;
 }
 // Scratch: per range two parts (a sequence cut at its start, one cut at its
 // end) of each unit: 8 x dim values and 8 (m, l) pairs; then the joins.
 inline size_t paged_scratch_bytes(const PagedPlan &n, int dim) {
-    return (size_t)2 * n.ranges * n.blocks * n.units_cta * (8 * dim + 16) * 4 + (size_t)n.ranges * 16;
+    return (size_t)2 * n.ranges * n.units * (8 * dim + 16) * 4 + (size_t)n.ranges * 16;
 }
+
+// Codes as (byte of a head, row, head), boxes of one head's bytes x 16 rows x
+// the CTA's heads; scales as (byte of 16, row, group of 16 bytes).
+struct PagedMaps {
+    CUtensorMap kc, ks, vc, vs;
+};
 
 struct PagedAttnParams {
     const uint16_t *q;       // BF16 [sequences][heads_q][dim], strides in elements
@@ -311,18 +337,19 @@ struct PagedAttnParams {
     const int32_t *seq_lens;
     int32_t sequences, heads_q, group, page_size;
     FastDiv page_div;
-    int32_t units_head, units_cta;
-    int32_t tile_shift;      // log2 of the tokens of a tile of the schedule
+    PagedPlan plan;
+    int32_t tma;             // page_size % 16 == 0 (16 tokens share a page) and 16-byte scale rows: tiles by TMA
     int32_t min_tiles;       // tiles a range has at least (but the last)
+    long long timeout;       // clock bound of a wait
     float scale;
     uint16_t *o;
     int64_t os_b, os_h;
     float *lse;              // nullptr, or [sequences][heads_q]
-    float *part_o;           // [2 ranges][units][8 * dim], fragment order
+    float *part_o;           // [2 ranges][units][8 * dim], in the order of the MMA's lanes
     float2 *part_ml;         // [2 ranges][units][8]
     int4 *joins;             // (sequence, first range, parts): by sequence, or by range if there are more sequences
     uint32_t *status;
 };
-cudaError_t launch_paged_attention(const PagedAttnParams &p, int dim, const PagedPlan &plan, cudaStream_t s);
+cudaError_t launch_paged_attention(const PagedAttnParams &p, const PagedMaps &maps, int dim, cudaStream_t s);
 
 }  // namespace nvfp4
