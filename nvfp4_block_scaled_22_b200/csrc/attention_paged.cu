@@ -235,7 +235,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
     __shared__ int masks[kPagedMaxStages][kWarps];
     __shared__ int rows_sh[kWarps * kTile];              // pool rows of a stage's tokens (copies without TMA)
-    __shared__ float ml[kWarps][8][2];
+    __shared__ float2 ml[kWarps][8];
     __shared__ int64_t warp_sums[kWarps + 1];
     __shared__ Cursor start_sh;
     grid_dependents_launch();
@@ -254,6 +254,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         const int per = (p.sequences + kThreads - 1) / kThreads;
         const int b0 = min(p.sequences, tid * per), b1 = min(p.sequences, b0 + per);
         int64_t mine = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int len = p.seq_lens[b];
             if ((len < 0 || len > p.capacity) && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
@@ -286,6 +287,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             if (tid == 0) p.joins[x] = make_int4(0, 0, 0, 0);
             __syncthreads();
         }
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int len = length_of(p, b), n = tiles_of(len, p.plan.tile_shift);
             if (at <= first && first < at + n && count > 0) {
@@ -370,6 +372,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     f.tokens = 0;
                 }
                 const int row = f.page * p.page_size + f.offset;
+#pragma unroll 1
                 for (int i = 0; i < f.n; ++i) {
                     const int src = (i << plan.parts_shift) + my_part;
                     const int r = __shfl_sync(0xFFFFFFFFu, row, src);
@@ -440,6 +443,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 lookup();
                 __syncwarp();
                 const uint32_t to = ring + stage * plan.stage_bytes;
+#pragma unroll 2
                 for (int n = lane; n < tokens_stage << piece_shift; n += 32) {
                     const int t = n >> piece_shift, x = n & ((1 << piece_shift) - 1);
                     const int h = x / S::kChunks, ch = x % S::kChunks;
@@ -452,6 +456,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         copy_async<16>(dst + v_codes, p.vc + src);
                     }
                 }
+#pragma unroll 2
                 for (int n = lane; n < tokens_stage << plan.heads_shift; n += 32) {
                     const int t = n >> plan.heads_shift, h = n & (heads_cta - 1);
                     const int r = rows_sh[t];
@@ -574,6 +579,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         const bool ends = in_seq <= left;                               // the sequence ends in this range
         const int n_tiles = ends ? in_seq : left;
         left -= n_tiles;
+#pragma unroll 1
         for (int tile = n_tiles; tile > 0; --tile) {
             // A wait that gives up leaves the CTA in step: its tiles then
             // count as empty, every barrier is still met.
@@ -713,81 +719,84 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             }
         }
 
-        // ---- end of this CTA's part of the sequence: join the unit's warps
+        // ---- end of this CTA's part of the sequence: join the unit's warps.
+        // Rolled loops through shared memory: this runs once a sequence, and
+        // straight-line code of it (130 KB with the loop above) cost more in
+        // instruction fetches than the work itself.
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) lsum[n] += __shfl_xor_sync(0xFFFFFFFFu, lsum[n], off);
-        float M[2] = {mp[0], mp[1]}, L[2] = {lsum[0], lsum[1]};
-        if (tw > 1) {
-            if (g == 0) {
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    ml[warp][2 * c + n][0] = mp[n];
-                    ml[warp][2 * c + n][1] = lsum[n];
-                }
-            }
-            unit_barrier(1 + unit_cta, 32 * tw);
-            const int w0 = unit_cta, step = kWarps >> plan.parts_shift;
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                for (int w = 0; w < tw; ++w) M[n] = fmaxf(M[n], ml[w0 + w * step][2 * c + n][0]);
-                L[n] = 0.0f;
-                for (int w = 0; w < tw; ++w) L[n] += ml[w0 + w * step][2 * c + n][1] * exp2_fast(ml[w0 + w * step][2 * c + n][0] - M[n]);
-            }
+        if (g == 0) {
+            ml[warp][2 * c] = make_float2(mp[0], lsum[0]);
+            ml[warp][2 * c + 1] = make_float2(mp[1], lsum[1]);
+        }
+        const int step = kWarps >> plan.parts_shift;                    // warps between two parts of a unit
+        auto unit_sync = [&]() {
+            if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
+            else warp_sync();
+        };
+        unit_sync();
+        float M[2] = {mp[0], mp[1]}, L[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int w = unit_cta; w < kWarps; w += step) {
+            M[0] = fmaxf(M[0], ml[w][2 * c].x);
+            M[1] = fmaxf(M[1], ml[w][2 * c + 1].x);
+        }
+#pragma unroll 1
+        for (int w = unit_cta; w < kWarps; w += step) {
+            const float2 v0 = ml[w][2 * c], v1 = ml[w][2 * c + 1];
+            L[0] += v0.y * exp2_fast(v0.x - M[0]);
+            L[1] += v1.y * exp2_fast(v1.x - M[1]);
+        }
+        {
             const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
             float *mine = sums + warp * (8 * kD) + lane;
 #pragma unroll
             for (int j = 0; j < S::kSteps; ++j)
 #pragma unroll
                 for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
-            unit_barrier(1 + unit_cta, 32 * tw);
         }
+        unit_sync();
         const bool whole = ends && starts_here;
-        const float *from = sums + unit_cta * (8 * kD) + lane;
         const int64_t slot = (int64_t)(2 * blockIdx.x + (starts_here ? 1 : 0)) * plan.units + unit;
+        float f[2];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) f[n] = whole ? (L[n] == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(L[n], *p.gv))) : 1.0f;
+        uint16_t *o = p.o + (int64_t)b * p.os_b + (int64_t)head0 * p.os_h + (kD / 8) * g;
         float *part_o = p.part_o + slot * (8 * kD) + lane;
-        const float gv = *p.gv;
+#pragma unroll 1
+        for (int j = part; j < S::kSteps; j += tw) {
+            const float *from = sums + unit_cta * (8 * kD) + 128 * j + lane;
+            float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int w = 0; w < tw; ++w, from += step * (8 * kD)) {
 #pragma unroll
-        for (int j = 0; j < S::kSteps; ++j) {
-            if ((j & (tw - 1)) != part) continue;
-            float r[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                r[n] = oacc[j][n];
-                if (tw > 1) {
-                    r[n] = 0.0f;
-                    for (int w = 0; w < tw; ++w) r[n] += from[w * (kWarps >> plan.parts_shift) * (8 * kD) + (4 * j + n) * 32];
-                }
+                for (int n = 0; n < 4; ++n) r[n] += from[32 * n];
             }
             if (whole) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    if (2 * c + n < heads) {
-                        const bool none = L[n] == 0.0f;
-                        const float lo = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n], L[n]), gv);
-                        const float hi = none ? 0.0f : __fdiv_rn(__fdiv_rn(r[n + 2], L[n]), gv);
-                        *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + 2 * c + n) * p.os_h +
-                                                      (kD / 8) * g + 2 * j) = bf16x2_from_f32(lo, hi);
-                    }
-                }
+                for (int n = 0; n < 2; ++n)
+                    if (2 * c + n < heads)
+                        *reinterpret_cast<uint32_t *>(o + (int64_t)(2 * c + n) * p.os_h + 2 * j) =
+                            bf16x2_from_f32(r[n] * f[n], r[n + 2] * f[n]);
             } else {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) part_o[(4 * j + n) * 32] = r[n];
+                for (int n = 0; n < 4; ++n) part_o[128 * j + 32 * n] = r[n];
             }
         }
         if (part == 0 && g == 0) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-                if (whole) {
-                    if (p.lse != nullptr && 2 * c + n < heads)
-                        p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] =
-                            L[n] == 0.0f ? -__int_as_float(0x7F800000) : (M[n] + log2f(L[n])) * kLn2;
-                } else {
+                if (!whole)
                     p.part_ml[slot * 8 + 2 * c + n] = make_float2(M[n], L[n]);
-                }
+                else if (p.lse != nullptr && 2 * c + n < heads)
+                    p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] =
+                        L[n] == 0.0f ? -__int_as_float(0x7F800000) : (M[n] + log2f(L[n])) * kLn2;
             }
         }
+        // The next sequence's sums are written only after every warp of the
+        // unit has met the first of the two barriers above again.
         if (left == 0) break;
         ++b;
         in_seq = tiles_of(length_of(p, b), plan.tile_shift);

@@ -306,7 +306,7 @@ inline PagedPlan paged_plan(int heads_q, int heads_kv, int dim) {
     const int heads = 1 << n.heads_shift, parts = 1 << n.parts_shift;
     const int groups = heads * (dim / 16) / 16 > 1 ? heads * (dim / 16) / 16 : 1;
     n.stage_bytes = (2 * parts * 16 * (heads * (dim / 2) + groups * 16) + 1023) / 1024 * 1024;
-    const int sums = parts > 1 ? 8 * 8 * dim * 4 : 0;                  // the warps' O
+    const int sums = 8 * 8 * dim * 4;                                  // the warps' O
     const int room = (dim == 256 ? kPagedSmem256 : kPagedSmem) - 1024 - sums;
     n.stages = room / n.stage_bytes < kPagedMaxStages ? room / n.stage_bytes : kPagedMaxStages;
     n.smem = 1024 + n.stages * n.stage_bytes + sums;
