@@ -110,7 +110,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -178,26 +178,24 @@ __device__ __forceinline__ void unit_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-    uint16_t d;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(d) : "r"(a));
-    return d;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
-    uint32_t d;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(d) : "r"(a));
-    return d;
-}
+__device__ __forceinline__ uint32_t lds16(const uint8_t *a) { return *reinterpret_cast<const uint16_t *>(a); }
+__device__ __forceinline__ uint32_t lds8(const uint8_t *a) { return *a; }
 // kWords (1, 2 or 4) words
 template <int kWords>
-__device__ __forceinline__ void lds_words(uint32_t a, uint32_t *d) {
-    if (kWords == 1)
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(d[0]) : "r"(a));
-    else if (kWords == 2)
-        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(d[0]), "=r"(d[1]) : "r"(a));
-    else
-        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]) : "r"(a));
+__device__ __forceinline__ void lds_words(const uint8_t *a, uint32_t *d) {
+    if (kWords == 1) {
+        d[0] = *reinterpret_cast<const uint32_t *>(a);
+    } else if (kWords == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(a);
+        d[0] = v.x;
+        d[1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(a);
+        d[0] = v.x;
+        d[1] = v.y;
+        d[2] = v.z;
+        d[3] = v.w;
+    }
 }
 
 // Length of sequence b (its tokens' table entries exist), and the tiles it
@@ -534,7 +532,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     int b = start_sh.b, in_seq = start_sh.tiles - start_sh.tile;        // tiles to the end of the sequence
     bool starts_here = start_sh.tile == 0;
     int left = count, stage = 0;
-    uint32_t phase = 0, at = ring;
+    uint32_t phase = 0;
+    const uint8_t *ring_at = smem_raw + (ring - smem_u32(smem_raw)), *at = ring_at;
     // the warps' O, where several share a unit's tokens
     float *sums = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
 
@@ -715,7 +714,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             if (++stage == plan.stages) {
                 stage = 0;
                 phase ^= 1u;
-                at = ring;
+                at = ring_at;
             }
         }
 
@@ -805,95 +804,127 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 }
 
 // Joins the parts of the sequences that were cut: blockIdx.x is the sequence
-// (or the range at whose end one is cut), blockIdx.y takes M-tiles of O^T (128
-// values of a unit).  Eight warps take the parts in turn, four at a time, each
-// with the running maximum and sum of the online softmax, and are joined in
-// shared memory; a part's maxima, sums and values are one round of loads.
-__global__ void __launch_bounds__(256) k_paged_combine(const __grid_constant__ PagedAttnParams p, int dim) {
-    __shared__ float2 ml[8][8];
-    __shared__ float4 sums[8][32];
+// (or the range at whose end one is cut); its items are the M-tiles of O^T of
+// each unit (128 values: 8 heads x 16 dims).  A warp takes four parts in one
+// round of loads -- their maxima, sums and values -- with the running maximum
+// and sum of the online softmax.  A sequence of few parts gets a warp an
+// item; one of many a CTA an item, whose warps deal the parts among them and
+// are joined in shared memory.
+constexpr int kJoinWarps = 16;
+constexpr int kFewParts = 16;
+
+struct JoinState {
+    float m, l;          // of head lane % 8
+    float4 a;            // values 4 lane .. + 3 of the M-tile
+};
+
+__device__ __forceinline__ JoinState join_parts(const PagedAttnParams &p, int dim, int x0, int pieces, int unit,
+                                                int j, int from, int step, int lane) {
+    // [n = 0 .. 3][lane of the MMA]: four neighbouring lanes are heads 0, 2,
+    // 4, 6 (n even) or 1, 3, 5, 7 (n odd)
+    const int odd = (lane >> 3) & 1, units = p.plan.units;
+    JoinState s = {kLowest, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+    // piece n: the first lies in the second slot of its range, the others in the first
+    auto slot = [&](int n) { return (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit; };
+#pragma unroll 1
+    for (int n0 = from; n0 < pieces; n0 += step) {
+        float4 o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(min(n0 + k, pieces - 1)) * (8 * dim) + 128 * j) + lane);
+        const int n = n0 + (lane >> 3);
+        float2 v = make_float2(kLowest, 0.0f);
+        if (n < pieces) v = __ldcg(p.part_ml + slot(n) * 8 + (lane & 7));
+        float top = fmaxf(s.m, v.x);
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
+        const float alpha = exp2_fast(s.m - top), w = n < pieces ? exp2_fast(v.x - top) : 0.0f;
+        s.m = top;
+        float wl = w * v.y;
+        wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 8);
+        wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 16);
+        s.l = s.l * alpha + wl;
+        s.a.x *= __shfl_sync(0xFFFFFFFFu, alpha, odd);
+        s.a.y *= __shfl_sync(0xFFFFFFFFu, alpha, 2 + odd);
+        s.a.z *= __shfl_sync(0xFFFFFFFFu, alpha, 4 + odd);
+        s.a.w *= __shfl_sync(0xFFFFFFFFu, alpha, 6 + odd);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float w0 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + odd), w1 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 2 + odd);
+            const float w2 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 4 + odd), w3 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 6 + odd);
+            if (n0 + k < pieces) {
+                s.a.x += o[k].x * w0;
+                s.a.y += o[k].y * w1;
+                s.a.z += o[k].z * w2;
+                s.a.w += o[k].w * w3;
+            }
+        }
+    }
+    return s;
+}
+
+// Values n = e and n = e + 2 (dims 2j, 2j + 1 of lane row g) of head h = 2c + e,
+// summed as lo and hi with the weights' sum L under the maximum M.
+__device__ __forceinline__ void join_store(const PagedAttnParams &p, int dim, int b, int unit, int j, int h, int g,
+                                           float M, float L, float lo, float hi) {
+    const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
+    const int head0 = hk * p.group + sub * 8;
+    if (h >= min(8, p.group - sub * 8)) return;
+    const float f = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(L, *p.gv));
+    *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + h) * p.os_h + (dim / 8) * g + 2 * j) =
+        bf16x2_from_f32(lo * f, hi * f);
+    if (j == 0 && g == 0 && p.lse != nullptr)
+        p.lse[(int64_t)b * p.heads_q + head0 + h] = L == 0.0f ? -__int_as_float(0x7F800000) : (M + log2f(L)) * kLn2;
+}
+
+__global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_constant__ PagedAttnParams p, int dim) {
+    __shared__ float2 ml[kJoinWarps][8];
+    __shared__ float sums[kJoinWarps][128];
+    grid_dependents_launch();
     grid_dependency_wait();
     const int4 join = p.joins[blockIdx.x];
     const int b = join.x, x0 = join.y, pieces = join.z;
     if (pieces <= 1) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = dim / 16, units = p.plan.units;
-    // values 4 lane .. + 3 of an M-tile: [n = 0 .. 3][lane of the MMA]; four
-    // neighbouring lanes are heads 0, 2, 4, 6 (n even) or 1, 3, 5, 7 (n odd)
-    const int odd = (lane >> 3) & 1;
-    for (int item = blockIdx.y; item < units * tiles; item += gridDim.y) {
-        const int unit = item / tiles, j = item - unit * tiles;
-        float m = kLowest, l = 0.0f;                                     // of head lane % 8
-        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int n0 = 4 * warp; n0 < pieces; n0 += 32) {
-            // piece n: the first lies in the second slot of its range, the others in the first
-            float4 o[4];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tiles = dim / 16, items = p.plan.units * tiles;
+    if (pieces <= kFewParts) {
+#pragma unroll 1
+        for (int item = blockIdx.y * kJoinWarps + warp; item < items; item += gridDim.y * kJoinWarps) {
+            const int unit = item / tiles, j = item - unit * tiles;
+            const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 0, 4, lane);
+            // lane 8 n + 4 k + ...: value n of lane rows and heads; n and n + 2 meet
+            __syncwarp();
+            *reinterpret_cast<float4 *>(&sums[warp][4 * lane]) = s.a;
+            if (lane < 8) ml[warp][lane] = make_float2(s.m, s.l);
+            __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int n = min(n0 + k, pieces - 1);
-                const int64_t slot = (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit;
-                o[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot * (8 * dim) + 128 * j) + lane);
-            }
-            const int n = n0 + (lane >> 3);
-            float2 v = make_float2(kLowest, 0.0f);
-            if (n < pieces) {
-                const int64_t slot = (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit;
-                v = __ldcg(p.part_ml + slot * 8 + (lane & 7));
-            }
-            float top = fmaxf(m, v.x);
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-            const float alpha = exp2_fast(m - top), w = n < pieces ? exp2_fast(v.x - top) : 0.0f;
-            m = top;
-            float wl = w * v.y;
-            wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 8);
-            wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 16);
-            l = l * alpha + wl;
-            a.x *= __shfl_sync(0xFFFFFFFFu, alpha, odd);
-            a.y *= __shfl_sync(0xFFFFFFFFu, alpha, 2 + odd);
-            a.z *= __shfl_sync(0xFFFFFFFFu, alpha, 4 + odd);
-            a.w *= __shfl_sync(0xFFFFFFFFu, alpha, 6 + odd);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float w0 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + odd), w1 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 2 + odd);
-                const float w2 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 4 + odd), w3 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 6 + odd);
-                if (n0 + k < pieces) {
-                    a.x += o[k].x * w0;
-                    a.y += o[k].y * w1;
-                    a.z += o[k].z * w2;
-                    a.w += o[k].w * w3;
-                }
+            for (int k = 0; k < 2; ++k) {
+                const int h = lane & 7, g = (lane >> 3) + 4 * k, at = (h & 1) * 32 + g * 4 + (h >> 1);
+                join_store(p, dim, b, unit, j, h, g, ml[warp][h].x, ml[warp][h].y, sums[warp][at], sums[warp][at + 64]);
             }
         }
-        sums[warp][lane] = a;
-        if (lane < 8) ml[warp][lane] = make_float2(m, l);
+        return;
+    }
+#pragma unroll 1
+    for (int item = blockIdx.y; item < items; item += gridDim.y) {
+        const int unit = item / tiles, j = item - unit * tiles;
+        const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 4 * warp, 4 * kJoinWarps, lane);
+        *reinterpret_cast<float4 *>(&sums[warp][4 * lane]) = s.a;
+        if (lane < 8) ml[warp][lane] = make_float2(s.m, s.l);
         __syncthreads();
-        const int tid = threadIdx.x;
         if (tid < 64) {
-            // one head and lane row g: values n = e and n = e + 2 (dims 2j, 2j + 1)
-            const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
-            const int head0 = hk * p.group + sub * 8, heads = min(8, p.group - sub * 8);
-            const int h = tid & 7, g = tid >> 3, e = h & 1, c = h >> 1;
-            const float *f = reinterpret_cast<const float *>(&sums[0][0]) + g * 4 + c;
+            const int h = tid & 7, g = tid >> 3, at = (h & 1) * 32 + g * 4 + (h >> 1);
             float M = kLowest, L = 0.0f, lo = 0.0f, hi = 0.0f;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) M = fmaxf(M, ml[n][h].x);
+            for (int n = 0; n < kJoinWarps; ++n) M = fmaxf(M, ml[n][h].x);
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < kJoinWarps; ++n) {
                 const float w = exp2_fast(ml[n][h].x - M);
                 L += w * ml[n][h].y;
-                lo += w * f[n * 128 + e * 32];
-                hi += w * f[n * 128 + (e + 2) * 32];
+                lo += w * sums[n][at];
+                hi += w * sums[n][at + 64];
             }
-            if (h < heads) {
-                const float gv = *p.gv;
-                lo = L == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(lo, L), gv);
-                hi = L == 0.0f ? 0.0f : __fdiv_rn(__fdiv_rn(hi, L), gv);
-                *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + h) * p.os_h +
-                                              (dim / 8) * g + 2 * j) = bf16x2_from_f32(lo, hi);
-                if (j == 0 && g == 0 && p.lse != nullptr)
-                    p.lse[(int64_t)b * p.heads_q + head0 + h] = L == 0.0f ? -__int_as_float(0x7F800000) : (M + log2f(L)) * kLn2;
-            }
+            join_store(p, dim, b, unit, j, h, g, M, L, lo, hi);
         }
         __syncthreads();
     }
@@ -940,13 +971,13 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p, const PagedMaps &ma
                     : dim == 128 ? launch_main<128>(p, maps, s)
                                  : launch_main<256>(p, maps, s);
     if (e != cudaSuccess) return e;
-    // the sequences that can be cut, and CTAs for about one wave of the device
+    // the sequences that can be cut; CTAs for a warp an item, and where the
+    // sequences are few, up to a CTA an item, within about two an SM
     const int joins = std::min(p.sequences, p.plan.ranges);
-    const int tiles = p.plan.units * (dim / 16);
-    const int per = std::max(1, (int)(((int64_t)joins * tiles + 1183) / 1184));
+    const int items = p.plan.units * (dim / 16);
+    const int y = std::min(items, std::max((items + kJoinWarps - 1) / kJoinWarps, 296 / joins));
     void *args[] = {const_cast<PagedAttnParams *>(&p), &dim};
-    return launch_dependent((const void *)k_paged_combine, dim3((unsigned)joins, (unsigned)((tiles + per - 1) / per)),
-                            256, 0, s, args);
+    return launch_dependent((const void *)k_paged_combine, dim3((unsigned)joins, (unsigned)y), 32 * kJoinWarps, 0, s, args);
 }
 
 }  // namespace nvfp4

@@ -283,7 +283,7 @@ constexpr int kPagedMinTiles = 1;
 constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
 constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
 #ifndef PU
-#define PU 8
+#define PU 4
 #endif
 struct PagedPlan {
     int units_head, units;                   // units of a KV head, of all
