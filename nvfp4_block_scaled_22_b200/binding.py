@@ -414,20 +414,27 @@ def nvfp4_attention_decode(q: torch.Tensor, k: NVFP4Tensor, v: NVFP4Tensor, head
 
 
 # -------------------------------------------------------- paged KV cache
+# These calls are made for every layer of every generated token, so that the
+# host's time counts: the checks are plain comparisons, and the current device
+# and stream are asked of torch's own bindings (a few hundred ns, against 7 us
+# through torch.cuda.current_stream()).
 def _require(ok: bool, what: str):
     if not ok:
         raise ValueError(what)
 
 
-def _together(device, **tensors):
-    """All of them are CUDA tensors of one device."""
-    for name, t in tensors.items():
-        _require(t is None or (t.is_cuda and t.device == device),
-                 f"{name} is not on {device}, the device of the first argument")
+def _current_device() -> int:
+    return torch._C._cuda_getDevice()
+
+
+def _current_stream(device: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 @contextlib.contextmanager
 def _switched(device, stream):
+    """The tensors' device and the given stream made current, so that outputs
+    and scratch belong to the stream the kernels run on."""
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -438,36 +445,62 @@ def _switched(device, stream):
                 yield
 
 
-def _on(device, stream):
-    """The tensors' device and the given stream made current, so that outputs
-    and scratch belong to the stream the kernels run on."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _switched(device, stream)
+def _workspace_of(workspace, device):
+    if workspace is None:
+        workspace = _default_ws.get(device.index) or default_workspace(device)
+    elif workspace.buf.device != device:
+        raise ValueError(f"workspace is not on {device}, the device of the first argument")
+    return workspace
 
 
-def _check_pool(k: NVFP4Tensor, v: NVFP4Tensor):
-    """The buffers hold what the C ABI is told (it cannot see their sizes)."""
-    for name, t in (("k_cache", k), ("v_cache", v)):
-        codes, scales = t.codes, t.scales
-        _require(t.layout == SF_LINEAR, f"{name}: the cache needs the linear scale layout")
-        _require(codes.dtype == torch.uint8 and codes.is_contiguous()
-                 and codes.numel() == t.rows * (t.cols // 2), f"{name}.codes: uint8 [rows, cols / 2]")
-        _require(scales.dtype == torch.uint8 and scales.is_contiguous()
-                 and scales.numel() == t.rows * (t.cols // 16), f"{name}.scales: uint8, rows * cols / 16")
-        _require(t.global_scale.dtype == torch.float32 and t.global_scale.numel() == 1,
-                 f"{name}.global_scale: float32, one element")
-        _together(k.codes.device, **{name + ".codes": codes, name + ".scales": scales,
-                                     name + ".global_scale": t.global_scale})
+def _pool_error(name, t, device):
+    """What is wrong with a cache's tensor."""
+    if t.layout != SF_LINEAR:
+        raise ValueError(f"{name}: the cache needs the linear scale layout")
+    for part, x, dtype, n in (("codes", t.codes, torch.uint8, t.rows * (t.cols // 2)),
+                              ("scales", t.scales, torch.uint8, t.rows * (t.cols // 16)),
+                              ("global_scale", t.global_scale, torch.float32, 1)):
+        if x.dtype != dtype or x.numel() != n or not x.is_contiguous():
+            raise ValueError(f"{name}.{part}: {dtype} of {n} elements, contiguous")
+        if x.device != device:
+            raise ValueError(f"{name} is not on {device}, the device of the first argument")
 
 
-def _check_rope(device, positions, table, tokens):
-    _require(table.dtype == torch.float32 and table.dim() == 3 and table.shape[2] == 2
-             and table.is_contiguous(), "table: float32 [positions, rotary_dim / 2, 2], contiguous")
-    _require(positions is not None and positions.dtype == torch.int32 and positions.dim() == 1
-             and positions.is_contiguous() and positions.numel() == tokens,
-             "positions: int32 [tokens], contiguous")
-    _together(device, table=table, positions=positions)
+def _pool_struct(name, t: NVFP4Tensor, device):
+    """C struct of a cache's tensor; its buffers hold what the C ABI is told
+    (which cannot see their sizes)."""
+    codes, scales, g, rows, cols, at = t.codes, t.scales, t.global_scale, t.rows, t.cols, device.index
+    if (t.layout != SF_LINEAR or codes.dtype is not torch.uint8 or scales.dtype is not torch.uint8
+            or g.dtype is not torch.float32 or codes.numel() != rows * (cols // 2)
+            or scales.numel() != rows * (cols // 16) or g.numel() != 1 or codes.get_device() != at
+            or scales.get_device() != at or g.get_device() != at or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        _pool_error(name, t, device)
+    return CTensor(codes.data_ptr(), scales.data_ptr(), g.data_ptr(), rows, cols, SF_LINEAR)
+
+
+def _check_index(name, t, device, n):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name}: int32, one dimension of {n}, contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} is not on {device}, the device of the first argument")
+
+
+def _check_table(table, device):
+    if table.dtype != torch.float32 or table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
+        raise ValueError("table: float32 [positions, rotary_dim / 2, 2], contiguous")
+    if table.device != device:
+        raise ValueError(f"table is not on {device}, the device of the first argument")
+
+
+def _check_heads(name, t, shape, device):
+    """A BF16 CUDA tensor of rows of heads, values of a head contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_cuda or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{name}: BF16 CUDA, three dimensions, innermost contiguous")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is not on {device}, the device of the first argument")
 
 
 def nvfp4_rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "plain",
@@ -490,13 +523,11 @@ def nvfp4_rope_table(inv_freq: torch.Tensor, positions: int, magnitude: float = 
     nvfp4_kv_write."""
     _require(inv_freq.dtype == torch.float64 and inv_freq.dim() == 1, "inv_freq: float64, one dimension")
     device = inv_freq.device if inv_freq.is_cuda else torch.device(device)
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
-    with _on(device, stream):
-        f = inv_freq.to(device).contiguous()
-        out = torch.empty((positions, f.numel(), 2), dtype=torch.float32, device=device)
+    with _switched(device, stream):
+        f = inv_freq.to(torch.device("cuda", _current_device())).contiguous()
+        out = torch.empty((positions, f.numel(), 2), dtype=torch.float32, device=f.device)
         _check(lib().nvfp4_rope_table(f.data_ptr(), 2 * f.numel(), first, positions, magnitude,
-                                      out.data_ptr(), _stream(None)), "nvfp4_rope_table")
+                                      out.data_ptr(), _current_stream(f.device.index)), "nvfp4_rope_table")
     return out
 
 
@@ -508,22 +539,27 @@ def nvfp4_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, in
     rotated, the rest copied.  ``inverse`` gives the gradient of x from that
     of the output.  ``out`` may be x itself; tokens at position -1 keep what
     ``out`` holds there."""
-    _require(x.dtype == torch.bfloat16 and x.dim() == 3 and x.is_cuda
-             and (x.stride(2) == 1 or x.shape[2] == 1), "x: BF16 CUDA [tokens, heads, head_dim], innermost contiguous")
+    _check_heads("x", x, None, None)
+    device = x.device
+    if stream is not None or device.index != _current_device():
+        with _switched(device, stream):
+            return nvfp4_rope(x, positions, table, interleaved, inverse, out, workspace)
     tokens, heads, dim = x.shape
-    _check_rope(x.device, positions, table, tokens)
-    _together(x.device, out=out)
-    with _on(x.device, stream):
-        if out is None:
-            out = torch.empty((tokens, heads, dim), dtype=torch.bfloat16, device=x.device)
-        _require(out.dtype == torch.bfloat16 and out.shape == x.shape
-                 and (out.stride(2) == 1 or dim == 1), "out: BF16 of x's shape, innermost contiguous")
-        ws = workspace or default_workspace(x.device)
-        _check(lib().nvfp4_rope(x.data_ptr(), x.stride(0), x.stride(1), tokens, heads, dim,
-                                positions.data_ptr(), table.data_ptr(), table.shape[0],
-                                2 * table.shape[1], int(interleaved), int(inverse), out.data_ptr(),
-                                out.stride(0), out.stride(1), ws.ptr, ws.nbytes, _stream(None)),
-               "nvfp4_rope")
+    _check_table(table, device)
+    _check_index("positions", positions, device, tokens)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _check_heads("out", out, x.shape, device)
+    ws = _workspace_of(workspace, device)
+    x_token, x_head, _ = x.stride()
+    out_token, out_head, _ = out.stride()
+    rows, pairs, _ = table.shape
+    st = lib().nvfp4_rope(x.data_ptr(), x_token, x_head, tokens, heads, dim, positions.data_ptr(),
+                          table.data_ptr(), rows, 2 * pairs, interleaved, inverse, out.data_ptr(),
+                          out_token, out_head, ws.ptr, ws.nbytes, _current_stream(device.index))
+    if st != 0:
+        raise NVFP4Error(st, "nvfp4_rope")
     return out
 
 
@@ -534,26 +570,29 @@ def nvfp4_kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cach
     """Quantize k and v (BF16 [tokens, heads, head_dim]) into rows ``slots``
     (int32, -1 = none) of the cache, under the caches' own tensor scales.
     With a ``table`` the keys are rotated to ``positions`` first."""
-    for name, t in (("k", k), ("v", v)):
-        _require(t.dtype == torch.bfloat16 and t.dim() == 3 and t.is_cuda and t.shape == k.shape
-                 and (t.stride(2) == 1 or t.shape[2] == 1),
-                 f"{name}: BF16 CUDA [tokens, heads, head_dim], innermost contiguous")
+    _check_heads("k", k, None, None)
+    device = k.device
+    if stream is not None or device.index != _current_device():
+        with _switched(device, stream):
+            return nvfp4_kv_write(k, v, slots, k_cache, v_cache, positions, table, interleaved, workspace)
+    _check_heads("v", v, k.shape, device)
     tokens, heads, dim = k.shape
-    _require(slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous()
-             and slots.numel() == tokens, "slots: int32 [tokens], contiguous")
-    _check_pool(k_cache, v_cache)
-    _together(k.device, v=v, slots=slots, k_cache=k_cache.codes)
+    _check_index("slots", slots, device, tokens)
+    tk, tv = _pool_struct("k_cache", k_cache, device), _pool_struct("v_cache", v_cache, device)
+    at, rows, pairs, pos = 0, 0, 0, 0
     if table is not None:
-        _check_rope(k.device, positions, table, tokens)
-    with _on(k.device, stream):
-        ws = workspace or default_workspace(k.device)
-        tk, tv = k_cache.c_struct(), v_cache.c_struct()
-        _check(lib().nvfp4_kv_write(k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0),
-                                    v.stride(1), tokens, heads, dim, slots.data_ptr(), C.byref(tk),
-                                    C.byref(tv), _ptr(positions if table is not None else None), _ptr(table),
-                                    0 if table is None else table.shape[0],
-                                    0 if table is None else 2 * table.shape[1], int(interleaved),
-                                    ws.ptr, ws.nbytes, _stream(None)), "nvfp4_kv_write")
+        _check_table(table, device)
+        _check_index("positions", positions, device, tokens)
+        rows, pairs, _ = table.shape
+        at, pos = table.data_ptr(), positions.data_ptr()
+    ws = _workspace_of(workspace, device)
+    k_token, k_head, _ = k.stride()
+    v_token, v_head, _ = v.stride()
+    st = lib().nvfp4_kv_write(k.data_ptr(), k_token, k_head, v.data_ptr(), v_token, v_head, tokens, heads,
+                              dim, slots.data_ptr(), tk, tv, pos, at, rows, 2 * pairs, interleaved, ws.ptr,
+                              ws.nbytes, _current_stream(device.index))
+    if st != 0:
+        raise NVFP4Error(st, "nvfp4_kv_write")
 
 
 def nvfp4_kv_read(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, slots: torch.Tensor,
@@ -561,24 +600,34 @@ def nvfp4_kv_read(k_cache: NVFP4Tensor, v_cache: NVFP4Tensor, slots: torch.Tenso
                   workspace: Workspace | None = None, stream=None):
     """Rows ``slots`` (int32, -1 = zeros) of the cache as BF16 [rows, heads *
     head_dim] pairs (k, v), restored as nvfp4_dequantize restores them."""
-    _require(slots.dtype == torch.int32 and slots.dim() == 1 and slots.is_contiguous() and slots.is_cuda,
-             "slots: int32 CUDA [rows], contiguous")
-    _check_pool(k_cache, v_cache)
+    if not slots.is_cuda:
+        raise ValueError("slots: int32 CUDA [rows]")
+    device = slots.device
+    if stream is not None or device.index != _current_device():
+        with _switched(device, stream):
+            return nvfp4_kv_read(k_cache, v_cache, slots, out, workspace)
     rows, cols = slots.numel(), k_cache.cols
-    _together(slots.device, k_cache=k_cache.codes)
-    with _on(slots.device, stream):
-        if out is None:
-            out = tuple(torch.empty((rows, cols), dtype=torch.bfloat16, device=slots.device) for _ in range(2))
+    _check_index("slots", slots, device, rows)
+    tk, tv = _pool_struct("k_cache", k_cache, device), _pool_struct("v_cache", v_cache, device)
+    if out is None:
+        out = (torch.empty((rows, cols), dtype=torch.bfloat16, device=device),
+               torch.empty((rows, cols), dtype=torch.bfloat16, device=device))
+    else:
         for t in out:
-            _require(t.dtype == torch.bfloat16 and t.shape == (rows, cols) and (t.stride(1) == 1 or cols == 1),
-                     "out: two BF16 [rows, heads * head_dim], innermost contiguous")
-            _together(slots.device, out=t)
-        ws = workspace or default_workspace(slots.device)
-        tk, tv = k_cache.c_struct(), v_cache.c_struct()
-        _check(lib().nvfp4_kv_read(C.byref(tk), C.byref(tv), slots.data_ptr(), rows, out[0].data_ptr(),
-                                   out[0].stride(0), out[1].data_ptr(), out[1].stride(0), ws.ptr,
-                                   ws.nbytes, _stream(None)), "nvfp4_kv_read")
+            if t.dtype != torch.bfloat16 or t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+                raise ValueError("out: two BF16 [rows, heads * head_dim], innermost contiguous")
+            if t.device != device:
+                raise ValueError(f"out is not on {device}, the device of the first argument")
+    yk, yv = out
+    ws = _workspace_of(workspace, device)
+    st = lib().nvfp4_kv_read(tk, tv, slots.data_ptr(), rows, yk.data_ptr(), yk.stride(0), yv.data_ptr(),
+                             yv.stride(0), ws.ptr, ws.nbytes, _current_stream(device.index))
+    if st != 0:
+        raise NVFP4Error(st, "nvfp4_kv_read")
     return out
+
+
+_scratch_bytes: dict[tuple[int, int, int], int] = {}     # by the head counts and head size
 
 
 def nvfp4_attention_decode_paged(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache: NVFP4Tensor,
@@ -591,36 +640,48 @@ def nvfp4_attention_decode_paged(q: torch.Tensor, k_cache: NVFP4Tensor, v_cache:
     [sequences].  Returns BF16 of q's shape, with ``return_lse`` also the
     float32 [sequences, heads_q] log of the summed exponentials.  The softmax
     scale defaults to 1 / sqrt(head_dim)."""
-    _require(q.dtype == torch.bfloat16 and q.dim() == 3 and q.is_cuda and q.stride(2) == 1,
-             "q: BF16 CUDA [sequences, heads_q, head_dim], innermost contiguous")
+    _check_heads("q", q, None, None)
+    device = q.device
+    if stream is not None or device.index != _current_device():
+        with _switched(device, stream):
+            return nvfp4_attention_decode_paged(q, k_cache, v_cache, heads_kv, block_table, seq_lens, page_size,
+                                                scale, out, return_lse, workspace)
     sequences, heads_q, dim = q.shape
-    _check_pool(k_cache, v_cache)
-    _require(heads_kv > 0 and k_cache.cols == heads_kv * dim, "the cache's columns are heads_kv * head_dim")
-    _require(block_table.dtype == torch.int32 and block_table.dim() == 2
-             and block_table.shape[0] == sequences and (block_table.stride(1) == 1 or block_table.shape[1] <= 1),
-             "block_table: int32 [sequences, pages], innermost contiguous")
-    _require(seq_lens.dtype == torch.int32 and seq_lens.dim() == 1 and seq_lens.is_contiguous()
-             and seq_lens.numel() == sequences, "seq_lens: int32 [sequences], contiguous")
-    _together(q.device, k_cache=k_cache.codes, block_table=block_table, seq_lens=seq_lens, out=out)
+    tk, tv = _pool_struct("k_cache", k_cache, device), _pool_struct("v_cache", v_cache, device)
+    if heads_kv <= 0 or k_cache.cols != heads_kv * dim:
+        raise ValueError("the cache's columns are heads_kv * head_dim")
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != sequences:
+        raise ValueError("block_table: int32 [sequences, pages]")
+    pages, (table_row, table_page) = block_table.shape[1], block_table.stride()
+    if pages > 1 and table_page != 1:
+        raise ValueError("block_table: innermost contiguous")
+    if block_table.device != device:
+        raise ValueError(f"block_table is not on {device}, the device of the first argument")
+    _check_index("seq_lens", seq_lens, device, sequences)
     if scale is None:
         scale = dim ** -0.5
-    with _on(q.device, stream):
-        if out is None:
-            out = torch.empty((sequences, heads_q, dim), dtype=torch.bfloat16, device=q.device)
-        _require(out.dtype == torch.bfloat16 and out.shape == q.shape and out.stride(2) == 1,
-                 "out: BF16 of q's shape, innermost contiguous")
-        lse = torch.empty((sequences, heads_q), dtype=torch.float32, device=q.device) if return_lse else None
-        # scratch of the call's own, from the allocator of the stream (or the
-        # graph being captured): calls on two streams do not share it
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_heads("out", out, q.shape, device)
+    lse = torch.empty((sequences, heads_q), dtype=torch.float32, device=device) if return_lse else None
+    # scratch of the call's own, from the allocator of the stream (or the
+    # graph being captured): calls on two streams do not share it
+    need = _scratch_bytes.get((heads_q, heads_kv, dim))
+    if need is None:
         need = int(lib().nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, dim))
-        scratch = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        ws = workspace or default_workspace(q.device)
-        tk, tv = k_cache.c_struct(), v_cache.c_struct()
-        _check(lib().nvfp4_attention_decode_paged(
-            q.data_ptr(), q.stride(0), q.stride(1), sequences, heads_q, C.byref(tk), C.byref(tv), heads_kv,
-            block_table.data_ptr(), block_table.stride(0), block_table.shape[1], seq_lens.data_ptr(),
-            page_size, float(scale), out.data_ptr(), out.stride(0), out.stride(1), _ptr(lse), ws.ptr,
-            ws.nbytes, _ptr(scratch), need, _stream(None)), "nvfp4_attention_decode_paged")
+        _scratch_bytes[heads_q, heads_kv, dim] = need
+    scratch = torch.empty(need, dtype=torch.uint8, device=device)
+    ws = _workspace_of(workspace, device)
+    q_seq, q_head, _ = q.stride()
+    out_seq, out_head, _ = out.stride()
+    st = lib().nvfp4_attention_decode_paged(
+        q.data_ptr(), q_seq, q_head, sequences, heads_q, tk, tv, heads_kv, block_table.data_ptr(), table_row,
+        pages, seq_lens.data_ptr(), page_size, scale, out.data_ptr(), out_seq, out_head,
+        0 if lse is None else lse.data_ptr(), ws.ptr, ws.nbytes, scratch.data_ptr(), need,
+        _current_stream(device.index))
+    if st != 0:
+        raise NVFP4Error(st, "nvfp4_attention_decode_paged")
     return (out, lse) if return_lse else out
 
 

@@ -851,8 +851,10 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
                         rest % 8 == 0 && (interleaved ? pairs % 4 == 0 : pairs % 8 == 0);
     const int64_t per_head = !pieces ? pairs + rest
                                      : (interleaved ? (rotary_dim + rest) / 8 : pairs / 8 + rest / 8);
+    const bool by_groups = pieces && !interleaved;
+    const int64_t groups = by_groups ? ceil_div(heads, kRopeHeads) : heads;
     // items are counted in 31 bits
-    if (tokens > INT32_MAX / per_head / heads) return NVFP4_ERR_SHAPE;
+    if (tokens > INT32_MAX / per_head / groups) return NVFP4_ERR_SHAPE;
     int sms = 0;
     st = current_device(&sms);
     if (st != NVFP4_OK) return st;
@@ -867,10 +869,10 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
     p.table = reinterpret_cast<const float2 *>(d_table);
     p.table_rows = table_rows;
     p.pairs = pairs;
-    p.dim = head_dim;
+    p.heads = heads;
     p.sign = inverse ? -1.0f : 1.0f;
-    p.items = (uint32_t)(tokens * heads * per_head);
-    p.per_token = fast_div((uint32_t)(heads * per_head));
+    p.items = (uint32_t)(tokens * groups * per_head);
+    p.per_token = fast_div((uint32_t)(groups * per_head));
     p.per_head = fast_div((uint32_t)per_head);
     p.status = static_cast<uint32_t *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -879,7 +881,7 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
     else if (interleaved)
         k_rope_interleaved<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
     else
-        k_rope_half<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+        k_rope_half<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p);
     return launched(cudaGetLastError());
 }
 
@@ -934,15 +936,22 @@ nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_hea
     p.table_rows = table_rows;
     p.pairs = rotary_dim / 2;
     p.interleaved = interleaved;
-    p.items = (uint32_t)(tokens * 2 * row_blocks);
-    p.per_token = fast_div((uint32_t)(2 * row_blocks));
-    p.per_head = fast_div((uint32_t)(head_dim / 16));
+    const bool whole = d_table != nullptr && !interleaved && p.pairs % 16 == 0;
+    const int64_t head_blocks = head_dim / 16, turned = whole ? p.pairs / 16 : 0;
+    const int64_t head_k = turned + ceil_div(head_blocks - 2 * turned, 2), head_v = ceil_div(head_blocks, 2);
+    p.head_blocks = (uint32_t)head_blocks;
+    p.k_items = (uint32_t)(heads * head_k);
+    p.items = (uint32_t)(tokens * heads * (head_k + head_v));
+    p.per_token = fast_div((uint32_t)(heads * (head_k + head_v)));
+    p.per_head_k = fast_div((uint32_t)head_k);
+    p.per_head_v = fast_div((uint32_t)head_v);
     p.status = static_cast<uint32_t *>(workspace);
-    const unsigned grid = (unsigned)ceil_div(p.items, 256);
+    // a wave of CTAs at most: each fills its tables once
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(p.items, 256), 8LL * sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (d_table == nullptr)
         k_kv_write<<<grid, 256, 0, s>>>(p);
-    else if (!interleaved && p.pairs % 16 == 0)
+    else if (whole)
         k_kv_write_half<<<grid, 256, 0, s>>>(p);
     else
         k_kv_write_any<<<grid, 256, 0, s>>>(p);
@@ -989,7 +998,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V, const i
     p.per_row = fast_div((uint32_t)(2 * row_blocks));
     p.row_blocks = (uint32_t)row_blocks;
     p.status = static_cast<uint32_t *>(workspace);
-    k_kv_read<<<(unsigned)ceil_div(p.items, 256), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    k_kv_read<<<(unsigned)ceil_div(p.items, 256 * kReadItems), 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
     return launched(cudaGetLastError());
 }
 

@@ -219,13 +219,17 @@ struct RopeParams {
     const int32_t *positions;
     const float2 *table;     // [table_rows][pairs] (cos, sin)
     int64_t table_rows;
-    int32_t pairs, dim;
+    int32_t pairs, heads;
     float sign;              // +1, or -1 for the inverse
     uint32_t items;          // work items (tokens x heads x items of a head)
     FastDiv per_token, per_head;
     uint32_t *status;
 };
-constexpr int kRopeItems = 4;   // items a thread takes, 256 apart
+constexpr int kRopeItems = 2;   // interleaved layout: items a thread takes, 256 apart
+#ifndef RH
+#define RH 4
+#endif
+constexpr int kRopeHeads = RH;   // half layout: heads an item takes
 __global__ void k_rope_table(const double *inv_freq, int32_t pairs, int64_t first, int64_t n,
                              double magnitude, float2 *table);
 __global__ void k_rope_half(RopeParams p);
@@ -246,9 +250,11 @@ struct KvWriteParams {
     int64_t table_rows;
     int32_t pairs;
     int32_t interleaved;
-    uint32_t items;          // tokens x (blocks of a K row + blocks of a V row)
-    FastDiv per_token;       // 2 x blocks of a row
-    FastDiv per_head;        // blocks of a head
+    // items of one or two blocks: tokens x (items of a K row + items of a V row)
+    uint32_t items, k_items; // all; of a K row
+    FastDiv per_token;       // items of a token
+    FastDiv per_head_k, per_head_v;
+    uint32_t head_blocks;
     uint32_t *status;
 };
 __global__ void k_kv_write(KvWriteParams p);
@@ -268,6 +274,7 @@ struct KvReadParams {
     uint32_t row_blocks;
     uint32_t *status;
 };
+constexpr int kReadItems = 4;   // blocks a thread takes
 __global__ void k_kv_read(KvReadParams p);
 
 // Decode attention over a paged cache (attention_paged.cu).

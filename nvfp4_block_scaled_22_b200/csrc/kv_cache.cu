@@ -8,13 +8,13 @@
 // scales; per 16-value block the steps of nvfp4_quantize with a supplied g,
 //   s = e4m3(RN(RN(amax / 6) g)),  e = s ? RN(g / s) : 0,
 //   code = e2m1(RN(x e)),
-// so the bytes are those of nvfp4_quantize of the (rotated) rows.  One thread
-// takes one block: 32 bytes in, 8 + 1 bytes out; neighbouring threads take
-// neighbouring blocks of a row.
+// so the bytes are those of nvfp4_quantize of the (rotated) rows; the two
+// divisions come from tables that a CTA fills once (they would be a third of
+// the instructions otherwise).  A thread takes two blocks at a time: a pair
+// that the half layout rotates into each other, or two neighbours.
 // k_kv_read: y = bf16(RN(e2m1 RN(s / g))), the steps of nvfp4_dequantize.
 //
-// Both are bound by memory (2.56 bytes a value; two IEEE divisions a block
-// are 2 to 3 instructions a value of the 14 that fit beside the copy).
+// Both are bound by memory (2.56 bytes a value).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -27,34 +27,46 @@ namespace nvfp4 {
 
 namespace {
 
-// The rotated block of 16 values of a key: `own` holds values 16b .. 16b + 15
-// of the head, x is the head.
-// kWhole: half layout and pairs % 16 == 0, so that the partners of a block
-// are one block; otherwise the partners are fetched one by one.
-template <bool kWhole>
-__device__ __forceinline__ void rotate_block(uint4 &a, uint4 &b, const uint16_t *x, int blk,
-                                             const KvWriteParams &p, int64_t pos) {
+struct Block {
+    uint4 lo, hi;            // 16 BF16 values
+};
+
+__device__ __forceinline__ Block load_block(const uint16_t *x) {
+    Block b;
+    b.lo = reinterpret_cast<const uint4 *>(x)[0];
+    b.hi = reinterpret_cast<const uint4 *>(x)[1];
+    return b;
+}
+
+// Values i .. i + 15 (a) and their partners (b), rotated by 16 table entries.
+__device__ __forceinline__ void rotate_blocks(Block &a, Block &b, const float2 *table) {
+    uint32_t w[8] = {a.lo.x, a.lo.y, a.lo.z, a.lo.w, a.hi.x, a.hi.y, a.hi.z, a.hi.w};
+    uint32_t u[8] = {b.lo.x, b.lo.y, b.lo.z, b.lo.w, b.hi.x, b.hi.y, b.hi.z, b.hi.w};
+    const float4 *cs = reinterpret_cast<const float4 *>(table);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float4 f = __ldg(cs + i);
+        float lo1, lo2, hi1, hi2;
+        rotate(bf16_lo(w[i]), bf16_lo(u[i]), f.x, f.y, lo1, lo2);
+        rotate(bf16_hi(w[i]), bf16_hi(u[i]), f.z, f.w, hi1, hi2);
+        w[i] = bf16x2_from_f32(lo1, hi1);
+        u[i] = bf16x2_from_f32(lo2, hi2);
+    }
+    a.lo = make_uint4(w[0], w[1], w[2], w[3]);
+    a.hi = make_uint4(w[4], w[5], w[6], w[7]);
+    b.lo = make_uint4(u[0], u[1], u[2], u[3]);
+    b.hi = make_uint4(u[4], u[5], u[6], u[7]);
+}
+
+// Block `blk` of head x rotated by itself: neighbouring pairs, or partners
+// fetched one by one (any pair count).
+__device__ __forceinline__ void rotate_alone(Block &a, const uint16_t *x, int blk, const KvWriteParams &p,
+                                             int64_t pos) {
     const int j0 = 16 * blk;
     if (j0 >= 2 * p.pairs) return;
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t w[8] = {a.lo.x, a.lo.y, a.lo.z, a.lo.w, a.hi.x, a.hi.y, a.hi.z, a.hi.w};
     const float2 *row = p.table + pos * p.pairs;
-    if (kWhole) {
-        const bool first = j0 < p.pairs;
-        const uint4 *partner = reinterpret_cast<const uint4 *>(x + (first ? j0 + p.pairs : j0 - p.pairs));
-        const uint4 c = partner[0], d = partner[1];
-        const uint32_t u[8] = {c.x, c.y, c.z, c.w, d.x, d.y, d.z, d.w};
-        const float4 *cs = reinterpret_cast<const float4 *>(row + (first ? j0 : j0 - p.pairs));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float4 f = __ldg(cs + i);
-            // first: y1 of (own, partner); second: y2 of (partner, own)
-            const float lo = first ? __fsub_rn(__fmul_rn(bf16_lo(w[i]), f.x), __fmul_rn(bf16_lo(u[i]), f.y))
-                                   : __fadd_rn(__fmul_rn(bf16_lo(w[i]), f.x), __fmul_rn(bf16_lo(u[i]), f.y));
-            const float hi = first ? __fsub_rn(__fmul_rn(bf16_hi(w[i]), f.z), __fmul_rn(bf16_hi(u[i]), f.w))
-                                   : __fadd_rn(__fmul_rn(bf16_hi(w[i]), f.z), __fmul_rn(bf16_hi(u[i]), f.w));
-            w[i] = bf16x2_from_f32(lo, hi);
-        }
-    } else if (p.interleaved) {
+    if (p.interleaved) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int pair = (j0 >> 1) + i;
@@ -76,54 +88,81 @@ __device__ __forceinline__ void rotate_block(uint4 &a, uint4 &b, const uint16_t 
                     const bool first = j < p.pairs;
                     const int pair = first ? j : j - p.pairs;
                     const float2 f = __ldg(row + pair);
-                    const float other = bf16_lo(x[first ? j + p.pairs : pair]);
-                    y[e] = first ? __fsub_rn(__fmul_rn(y[e], f.x), __fmul_rn(other, f.y))
-                                 : __fadd_rn(__fmul_rn(y[e], f.x), __fmul_rn(other, f.y));
+                    float y1, y2;
+                    if (first) {
+                        rotate(y[e], bf16_lo(x[j + p.pairs]), f.x, f.y, y1, y2);
+                        y[e] = y1;
+                    } else {
+                        rotate(bf16_lo(x[pair]), y[e], f.x, f.y, y1, y2);
+                        y[e] = y2;
+                    }
                 }
             }
             w[i] = bf16x2_from_f32(y[0], y[1]);
         }
     }
-    a = make_uint4(w[0], w[1], w[2], w[3]);
-    b = make_uint4(w[4], w[5], w[6], w[7]);
+    a.lo = make_uint4(w[0], w[1], w[2], w[3]);
+    a.hi = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// kRope: 0 no rotation, 1 whole partner blocks, 2 any.
+// kRope: 0 no rotation, 1 half layout with whole partner blocks (pairs % 16
+// == 0), 2 any other.
 template <int kRope>
 __device__ __forceinline__ void kv_write_body(const KvWriteParams &p) {
-    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
-    if (item >= p.items) return;
-    const uint32_t t = quotient(item, p.per_token);
-    uint32_t blk = item - t * p.per_token.d;               // block of the K row, then of the V row
-    const int64_t row = pool_row(p.slots[t], p.pool_rows, p.status);
-    if (row < 0) return;
-    const uint32_t row_blocks = p.per_token.d >> 1;
-    const bool is_v = blk >= row_blocks;
-    if (is_v) blk -= row_blocks;
-    const uint32_t h = quotient(blk, p.per_head), b = blk - h * p.per_head.d;
-    int64_t pos = 0;
-    if (kRope != 0) {
+    __shared__ EncodeTables tables[2];
+    const float gk = *p.gk, gv = *p.gv;
+    fill_tables(tables[0], gk);
+    fill_tables(tables[1], gv);
+    __syncthreads();
+    // items of a head: pairs of rotated blocks (kRope 1), then two neighbours at a time
+    const int turned = kRope == 1 ? p.pairs >> 4 : 0;
+    const int head_blocks = (int)p.head_blocks;
+#pragma unroll 1
+    for (uint32_t item = blockIdx.x * 256u + threadIdx.x; item < p.items; item += gridDim.x * 256u) {
+        const uint32_t t = quotient(item, p.per_token);
+        uint32_t rest = item - t * p.per_token.d;                   // of the K row, then of the V row
+        const bool is_v = rest >= p.k_items;
+        if (is_v) rest -= p.k_items;
+        const uint32_t h = quotient(rest, is_v ? p.per_head_v : p.per_head_k);
+        const int i = (int)(rest - h * (is_v ? p.per_head_v.d : p.per_head_k.d));
+        // the values are fetched before the slot is known to be one
+        const int32_t slot = p.slots[t], position = kRope != 0 ? p.positions[t] : 0;
+        const uint16_t *x = is_v ? p.v + (int64_t)t * p.vs_t + (int64_t)h * p.vs_h
+                                 : p.k + (int64_t)t * p.ks_t + (int64_t)h * p.ks_h;
+        int b0, b1;
+        if (kRope == 1 && !is_v && i < turned) {
+            b0 = i;
+            b1 = i + turned;
+        } else {
+            b0 = is_v ? 2 * i : 2 * turned + 2 * (i - turned);
+            b1 = b0 + 1 < head_blocks ? b0 + 1 : -1;
+        }
+        Block a = load_block(x + 16 * b0), b = a;
+        if (b1 >= 0) b = load_block(x + 16 * b1);
+        const int64_t row = pool_row(slot, p.pool_rows, p.status);
         // a token whose position has no table row is not written at all
-        pos = rope_row(p.positions[t], p.table_rows, p.status);
-        if (pos < 0) return;
+        const int64_t pos = row >= 0 && kRope != 0 ? rope_row(position, p.table_rows, p.status) : 0;
+        if (row < 0 || pos < 0) continue;
+        if (!is_v) {
+            if (kRope == 1 && i < turned) rotate_blocks(a, b, p.table + pos * p.pairs + 16 * i);
+            if (kRope == 2) {
+                rotate_alone(a, x, b0, p, pos);
+                if (b1 >= 0) rotate_alone(b, x, b1, p, pos);
+            }
+        }
+        const float g = is_v ? gv : gk;
+        const EncodeTables &tab = tables[is_v ? 1 : 0];
+        const EncodeBlockOut ea = encode_block(a.lo, a.hi, g, tab), eb = encode_block(b.lo, b.hi, g, tab);
+        if (!ea.finite || !eb.finite) set_status(p.status, ST_NONFINITE);
+        uint8_t *c = (is_v ? p.vc : p.kc) + row * p.row_codes + (int64_t)h * head_blocks * 8;
+        uint8_t *sc = (is_v ? p.vs : p.ks) + row * p.row_scales + (int64_t)h * head_blocks;
+        *reinterpret_cast<uint2 *>(c + 8 * b0) = ea.codes;
+        sc[b0] = (uint8_t)ea.scale;
+        if (b1 >= 0) {
+            *reinterpret_cast<uint2 *>(c + 8 * b1) = eb.codes;
+            sc[b1] = (uint8_t)eb.scale;
+        }
     }
-    const uint16_t *x = is_v ? p.v + (int64_t)t * p.vs_t + (int64_t)h * p.vs_h
-                             : p.k + (int64_t)t * p.ks_t + (int64_t)h * p.ks_h;
-    uint4 w0 = reinterpret_cast<const uint4 *>(x + 16 * b)[0];
-    uint4 w1 = reinterpret_cast<const uint4 *>(x + 16 * b)[1];
-    if (kRope != 0 && !is_v) rotate_block<kRope == 1>(w0, w1, x, (int)b, p, pos);
-    const uint32_t bits = block_amax_bits(w0, w1);
-    if (bits > 0x7F7FFFFFu) set_status(p.status, ST_NONFINITE);
-    const float g = is_v ? *p.gv : *p.gk;
-    const uint32_t s = e4m3_from_f32(__fmul_rn(__fdiv_rn(__uint_as_float(bits), 6.0f), g));
-    const float e = (s & 0x7Fu) == 0u ? 0.0f : __fdiv_rn(g, f32_from_e4m3(s & 0x7Fu));
-    uint2 codes;
-    codes.x = encode8(w0.x, w0.y, w0.z, w0.w, e);
-    codes.y = encode8(w1.x, w1.y, w1.z, w1.w, e);
-    uint8_t *c = (is_v ? p.vc : p.kc) + row * p.row_codes;
-    uint8_t *sc = (is_v ? p.vs : p.ks) + row * p.row_scales;
-    reinterpret_cast<uint2 *>(c)[blk] = codes;
-    sc[blk] = (uint8_t)s;
 }
 
 }  // namespace
@@ -132,28 +171,48 @@ __global__ void __launch_bounds__(256) k_kv_write(KvWriteParams p) { kv_write_bo
 __global__ void __launch_bounds__(256) k_kv_write_half(KvWriteParams p) { kv_write_body<1>(p); }
 __global__ void __launch_bounds__(256) k_kv_write_any(KvWriteParams p) { kv_write_body<2>(p); }
 
+// Four blocks a thread, 256 apart, loaded before the first is stored.
 __global__ void __launch_bounds__(256) k_kv_read(KvReadParams p) {
-    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
-    if (item >= p.items) return;
-    const uint32_t r = quotient(item, p.per_row);
-    uint32_t blk = item - r * p.per_row.d;
-    const bool is_v = blk >= p.row_blocks;
-    if (is_v) blk -= p.row_blocks;
-    const int64_t row = pool_row(p.slots[r], p.pool_rows, p.status);
-    uint32_t o[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (row >= 0) {
-        const uint2 c = __ldg(reinterpret_cast<const uint2 *>((is_v ? p.vc : p.kc) + row * p.row_codes) + blk);
-        const uint32_t s = __ldg((is_v ? p.vs : p.ks) + row * p.row_scales + blk);
-        const float d = __fdiv_rn(f32_from_e4m3(s), is_v ? *p.gv : *p.gk);
+    const uint32_t base = blockIdx.x * (256u * kReadItems) + threadIdx.x;
+    uint2 c[kReadItems];
+    uint32_t s[kReadItems];
+    uint16_t *y[kReadItems];
+    bool is_v[kReadItems];
+#pragma unroll
+    for (int n = 0; n < kReadItems; ++n) {
+        const uint32_t item = base + 256u * n;
+        y[n] = nullptr;
+        c[n] = make_uint2(0u, 0u);
+        s[n] = 0u;
+        is_v[n] = false;
+        if (item < p.items) {
+            const uint32_t r = quotient(item, p.per_row);
+            uint32_t blk = item - r * p.per_row.d;
+            is_v[n] = blk >= p.row_blocks;
+            if (is_v[n]) blk -= p.row_blocks;
+            const int64_t row = pool_row(p.slots[r], p.pool_rows, p.status);
+            y[n] = (is_v[n] ? p.yv + (int64_t)r * p.ldv : p.yk + (int64_t)r * p.ldk) + 16 * (int64_t)blk;
+            if (row >= 0) {
+                c[n] = __ldg(reinterpret_cast<const uint2 *>((is_v[n] ? p.vc : p.kc) + row * p.row_codes) + blk);
+                s[n] = __ldg((is_v[n] ? p.vs : p.ks) + row * p.row_scales + blk);
+            }
+        }
+    }
+    const float gk = *p.gk, gv = *p.gv;
+#pragma unroll
+    for (int n = 0; n < kReadItems; ++n) {
+        if (y[n] == nullptr) continue;
+        // codes and scale 0 (no row): zeros
+        const float d = __fdiv_rn(f32_from_e4m3(s[n]), is_v[n] ? gv : gk);
+        uint32_t o[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = ((i < 4 ? c.x : c.y) >> (8 * (i & 3))) & 0xFFu;
+            const uint32_t byte = ((i < 4 ? c[n].x : c[n].y) >> (8 * (i & 3))) & 0xFFu;
             const float2 f = f32x2_from_f16x2(f16x2_from_e2m1x2(byte));
             o[i] = bf16x2_from_f32(__fmul_rn(f.x, d), __fmul_rn(f.y, d));
         }
+        store_32b(y[n], make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), p.vec32 != 0);
     }
-    uint16_t *y = (is_v ? p.yv + (int64_t)r * p.ldv : p.yk + (int64_t)r * p.ldk) + 16 * (int64_t)blk;
-    store_32b(y, make_uint4(o[0], o[1], o[2], o[3]), make_uint4(o[4], o[5], o[6], o[7]), p.vec32 != 0);
 }
 
 }  // namespace nvfp4

@@ -32,74 +32,117 @@ __global__ void __launch_bounds__(256) k_rope_table(const double *__restrict__ i
     }
 }
 
-// Half layout, 8 pairs an item (two 16-byte pieces of a head, one table
-// row's 64 bytes), then the 8-value pieces behind the rotated part.
+// Where an item lies: a token's position row (-1: left alone), and the item's
+// piece of a head.
+struct RopeItem {
+    int64_t row;
+    const uint16_t *x;
+    uint16_t *y;
+    uint32_t piece;
+};
+
+__device__ __forceinline__ RopeItem rope_item(const RopeParams &p, uint32_t item) {
+    const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
+    const uint32_t h = quotient(in_t, p.per_head);
+    RopeItem r;
+    r.row = rope_row(p.positions[t], p.table_rows, p.status);
+    r.x = p.x + (int64_t)t * p.xs_t + (int64_t)h * p.xs_h;
+    r.y = p.y + (int64_t)t * p.ys_t + (int64_t)h * p.ys_h;
+    r.piece = in_t - h * p.per_head.d;
+    return r;
+}
+
+// Half layout: an item is 8 pairs (two 16-byte pieces) of kRopeHeads heads
+// of a token, which share 64 bytes of the table; then the 8-value pieces
+// behind the rotated part.  With an item a head, the table took twice the
+// L1 traffic of the values (58 us against 50 at 8192 x 72 x 128).  All heads
+// are loaded before one is stored (y may be x, so that the compiler would
+// not).
 __global__ void __launch_bounds__(256) k_rope_half(RopeParams p) {
-    const uint32_t base = blockIdx.x * (256u * kRopeItems) + threadIdx.x;
+    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    if (item >= p.items) return;
+    const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
+    const uint32_t group = quotient(in_t, p.per_head), piece = in_t - group * p.per_head.d;
     const uint32_t pair_items = (uint32_t)p.pairs >> 3;
+    const int h0 = (int)group * kRopeHeads;
+    const bool turned = piece < pair_items;
+    const uint32_t at = turned ? 8 * piece : 2 * p.pairs + 8 * (piece - pair_items);
+    const uint16_t *x = p.x + (int64_t)t * p.xs_t + (int64_t)h0 * p.xs_h + at;
+    uint16_t *y = p.y + (int64_t)t * p.ys_t + (int64_t)h0 * p.ys_h + at;
+    const int32_t position = p.positions[t];
+    uint4 a[kRopeHeads], b[kRopeHeads];
 #pragma unroll
-    for (int n = 0; n < kRopeItems; ++n) {
-        const uint32_t item = base + 256u * n;
-        if (item >= p.items) return;
-        const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
-        const uint32_t h = quotient(in_t, p.per_head), c = in_t - h * p.per_head.d;
-        const int64_t pos = rope_row(p.positions[t], p.table_rows, p.status);
-        if (pos < 0) continue;
-        const uint16_t *x = p.x + (int64_t)t * p.xs_t + (int64_t)h * p.xs_h;
-        uint16_t *y = p.y + (int64_t)t * p.ys_t + (int64_t)h * p.ys_h;
-        if (c < pair_items) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(x + 8 * c);
-            const uint4 b = *reinterpret_cast<const uint4 *>(x + p.pairs + 8 * c);
-            const float4 *cs = reinterpret_cast<const float4 *>(p.table + pos * p.pairs + 8 * c);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    for (int h = 0; h < kRopeHeads; ++h) {
+        a[h] = b[h] = make_uint4(0u, 0u, 0u, 0u);
+        if (h0 + h < p.heads) {
+            a[h] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * p.xs_h);
+            if (turned) b[h] = *reinterpret_cast<const uint4 *>(x + (int64_t)h * p.xs_h + p.pairs);
+        }
+    }
+    const int64_t row = rope_row(position, p.table_rows, p.status);
+    if (row < 0) return;
+    if (turned) {
+        const float4 *cs = reinterpret_cast<const float4 *>(p.table + row * p.pairs + 8 * piece);
+        float4 f[4];                                     // cos, sin of two pairs
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[i] = __ldg(cs + i);
+            f[i].y *= p.sign;
+            f[i].w *= p.sign;
+        }
+#pragma unroll
+        for (int h = 0; h < kRopeHeads; ++h) {
+            const uint32_t aw[4] = {a[h].x, a[h].y, a[h].z, a[h].w}, bw[4] = {b[h].x, b[h].y, b[h].z, b[h].w};
             uint32_t ya[4], yb[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldg(cs + i);          // cos, sin of two pairs
                 float lo1, lo2, hi1, hi2;
-                rotate(bf16_lo(aw[i]), bf16_lo(bw[i]), f.x, p.sign * f.y, lo1, lo2);
-                rotate(bf16_hi(aw[i]), bf16_hi(bw[i]), f.z, p.sign * f.w, hi1, hi2);
+                rotate(bf16_lo(aw[i]), bf16_lo(bw[i]), f[i].x, f[i].y, lo1, lo2);
+                rotate(bf16_hi(aw[i]), bf16_hi(bw[i]), f[i].z, f[i].w, hi1, hi2);
                 ya[i] = bf16x2_from_f32(lo1, hi1);
                 yb[i] = bf16x2_from_f32(lo2, hi2);
             }
-            *reinterpret_cast<uint4 *>(y + 8 * c) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
-            *reinterpret_cast<uint4 *>(y + p.pairs + 8 * c) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
-        } else {
-            const uint32_t at = 2 * p.pairs + 8 * (c - pair_items);
-            *reinterpret_cast<uint4 *>(y + at) = *reinterpret_cast<const uint4 *>(x + at);
+            if (h0 + h < p.heads) {
+                *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h) = make_uint4(ya[0], ya[1], ya[2], ya[3]);
+                *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h + p.pairs) = make_uint4(yb[0], yb[1], yb[2], yb[3]);
+            }
         }
+    } else {
+#pragma unroll
+        for (int h = 0; h < kRopeHeads; ++h)
+            if (h0 + h < p.heads) *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h) = a[h];
     }
 }
 
 // Interleaved layout, 8 values (4 pairs) an item.
 __global__ void __launch_bounds__(256) k_rope_interleaved(RopeParams p) {
     const uint32_t base = blockIdx.x * (256u * kRopeItems) + threadIdx.x;
+    RopeItem it[kRopeItems];
+    uint4 a[kRopeItems];
 #pragma unroll
     for (int n = 0; n < kRopeItems; ++n) {
-        const uint32_t item = base + 256u * n;
-        if (item >= p.items) return;
-        const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
-        const uint32_t h = quotient(in_t, p.per_head), c = in_t - h * p.per_head.d;
-        const int64_t pos = rope_row(p.positions[t], p.table_rows, p.status);
-        if (pos < 0) continue;
-        const uint4 a = *reinterpret_cast<const uint4 *>(p.x + (int64_t)t * p.xs_t + (int64_t)h * p.xs_h + 8 * c);
-        uint4 *y = reinterpret_cast<uint4 *>(p.y + (int64_t)t * p.ys_t + (int64_t)h * p.ys_h + 8 * c);
-        if (4 * c < (uint32_t)p.pairs) {
-            const float4 *cs = reinterpret_cast<const float4 *>(p.table + pos * p.pairs + 4 * c);
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-            uint32_t o[4];
+        it[n].row = -1;
+        if (base + 256u * n < p.items) it[n] = rope_item(p, base + 256u * n);
+        if (it[n].row >= 0) a[n] = *reinterpret_cast<const uint4 *>(it[n].x + 8 * it[n].piece);
+    }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 f = __ldg(cs + (i >> 1));
-                float y1, y2;
-                rotate(bf16_lo(aw[i]), bf16_hi(aw[i]), (i & 1) ? f.z : f.x,
-                       p.sign * ((i & 1) ? f.w : f.y), y1, y2);
-                o[i] = bf16x2_from_f32(y1, y2);
-            }
-            *y = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-            *y = a;
+    for (int n = 0; n < kRopeItems; ++n) {
+        if (it[n].row < 0) continue;
+        uint4 y = a[n];
+        if (4 * it[n].piece < (uint32_t)p.pairs) {
+            const float4 *cs = reinterpret_cast<const float4 *>(p.table + it[n].row * p.pairs + 4 * it[n].piece);
+            const float4 f0 = __ldg(cs), f1 = __ldg(cs + 1);
+            float lo, hi;
+            rotate(bf16_lo(a[n].x), bf16_hi(a[n].x), f0.x, p.sign * f0.y, lo, hi);
+            y.x = bf16x2_from_f32(lo, hi);
+            rotate(bf16_lo(a[n].y), bf16_hi(a[n].y), f0.z, p.sign * f0.w, lo, hi);
+            y.y = bf16x2_from_f32(lo, hi);
+            rotate(bf16_lo(a[n].z), bf16_hi(a[n].z), f1.x, p.sign * f1.y, lo, hi);
+            y.z = bf16x2_from_f32(lo, hi);
+            rotate(bf16_lo(a[n].w), bf16_hi(a[n].w), f1.z, p.sign * f1.w, lo, hi);
+            y.w = bf16x2_from_f32(lo, hi);
         }
+        *reinterpret_cast<uint4 *>(it[n].y + 8 * it[n].piece) = y;
     }
 }
 
