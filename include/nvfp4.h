@@ -448,7 +448,8 @@ NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *
  * outside of the pool take no part and are recorded alike.
  * q, o  : BF16 [sequences][heads_q][head_dim], strides in elements, multiples
  *         of 8; 16-byte aligned.  head_dim = K->cols / heads_kv: 64, 128, 256.
- * page_size: any; K->rows a multiple of it and below 2^31.
+ * page_size: any; K->rows a multiple of it and below 2^31.  table_pages *
+ *   page_size < 2^31 - 1024, sequences * (table_pages * page_size / 16 + 1) < 2^31.
  * scratch: nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, head_dim)
  *   bytes, 16-byte aligned, of any content; calls that may run at the same
  *   time need scratch of their own (they may share the workspace, of which

@@ -60,8 +60,12 @@ constexpr float kLowest = -3.402823466e38f;
 constexpr float kOffset = 6.0f;      // m' is this much below the reference
 constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' moves
 
-constexpr int kWarps = 8;            // warps that compute; one more brings the tiles in
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 8;            // warps that compute
+#ifndef NP
+#define NP 2
+#endif
+constexpr int kProducers = NP;       // warps that bring the tiles in, stages in turn
+constexpr int kThreads = 32 * (kWarps + kProducers);
 constexpr int kTile = 16;            // tokens of a warp's tile
 
 template <int kD>
@@ -157,6 +161,17 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return d;
 }
 
+template <int kN>
+struct Parts {
+    static constexpr int value = kN;
+};
+
+// log of a sum l of 2^(x - m), natural; lg2.approx is off by at most 2^-22
+// (l is 0 or at least 1)
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l == 0.0f ? -__int_as_float(0x7F800000) : (m + __log2f(l)) * kLn2;
+}
+
 // (a & m) | (b & ~m), m = 0x0F0F0F0F
 __device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -201,11 +216,41 @@ __device__ __forceinline__ void lds_words(const uint8_t *a, uint32_t *d) {
 // Length of sequence b (its tokens' table entries exist), and the tiles it
 // counts in the schedule.
 __device__ __forceinline__ int length_of(const PagedAttnParams &p, int b) {
-    const int len = p.seq_lens[b];
-    return len < 0 ? 0 : min(len, p.capacity);
+    const int len = __ldg(p.seq_lens + b);
+    return min(max(len, 0), p.capacity);
 }
 __device__ __forceinline__ int tiles_of(int len, int tile_shift) {
     return max(1, (int)(((uint32_t)len + (1u << tile_shift) - 1u) >> tile_shift));
+}
+
+// The list of tiles cut into ranges, the first `longer` of them one longer
+// than the others (fewer tiles than CTAs: ranges of one tile).
+struct Ranges {
+    uint32_t length, longer, n, total;
+    __device__ __forceinline__ uint32_t first(uint32_t x) const {
+        return x >= n ? total : x * length + min(x, longer);
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t tile) const {       // range of a tile
+        const uint32_t split = longer * (length + 1);
+        return tile < split ? tile / (length + 1) : longer + (tile - split) / length;
+    }
+};
+__device__ __forceinline__ Ranges ranges_of(uint32_t total, uint32_t ctas) {
+    Ranges r;
+    r.total = total;
+    r.n = min(total, ctas);
+    r.length = total / r.n;
+    r.longer = total - r.n * r.length;
+    return r;
+}
+
+constexpr int kWarpSchedule = 128;   // up to this many sequences each warp works the schedule out for itself
+
+// What the joining kernel has to know of a sequence that starts in this range.
+__device__ __forceinline__ void write_join(const PagedAttnParams &p, const Ranges &r, int b, uint32_t at, int tiles) {
+    const int x = (int)blockIdx.x, pieces = (int)r.of(at + tiles - 1) - x + 1;
+    if (p.sequences <= (int)gridDim.x) p.joins[b] = make_int4(b, x, pieces, 0);
+    else if (pieces > 1) p.joins[x] = make_int4(b, x, pieces, 0);
 }
 
 // A position in the list of tiles.
@@ -232,9 +277,9 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
     __shared__ int masks[kPagedMaxStages][kWarps];
-    __shared__ int rows_sh[kWarps * kTile];              // pool rows of a stage's tokens (copies without TMA)
+    __shared__ int rows_sh[kProducers][kWarps * kTile];  // pool rows of a stage's tokens (copies without TMA)
     __shared__ float2 ml[kWarps][8];
-    __shared__ int64_t warp_sums[kWarps + 1];
+    __shared__ uint32_t warp_sums[kWarps + kProducers];
     __shared__ Cursor start_sh;
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -246,65 +291,102 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     // what is read from here on may be the result of the kernels before
     grid_dependency_wait();
 
-    // ---- schedule: this CTA's range of the tiles
+    const float gk = __ldg(p.gk);        // used after the schedule, which hides the load
+
+    // ---- schedule: this CTA's range of the tiles, and where it starts
+    Cursor start;
     int count;
-    {
-        const int per = (p.sequences + kThreads - 1) / kThreads;
-        const int b0 = min(p.sequences, tid * per), b1 = min(p.sequences, b0 + per);
-        int64_t mine = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const int len = p.seq_lens[b];
-            if ((len < 0 || len > p.capacity) && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
-            mine += tiles_of(length_of(p, b), p.plan.tile_shift);
+    if (p.sequences <= kWarpSchedule) {
+        // every warp for itself: a lane holds neighbouring sequences
+        const int per = (p.sequences + 31) >> 5, b0 = lane * per;
+        int lens[kWarpSchedule / 32];
+        uint32_t mine = 0;
+        bool wrong = false;
+#pragma unroll
+        for (int n = 0; n < kWarpSchedule / 32; ++n) {
+            lens[n] = 0;
+            if (n < per && b0 + n < p.sequences) {
+                const int len = __ldg(p.seq_lens + b0 + n);
+                wrong |= len < 0 || len > p.capacity;
+                lens[n] = min(max(len, 0), p.capacity);
+                mine += tiles_of(lens[n], p.plan.tile_shift);
+            }
         }
-        int64_t upto = mine;
+        if (wrong && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
+        uint32_t upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+            if (lane >= off) upto += v;
+        }
+        const Ranges ranges = ranges_of(__shfl_sync(0xFFFFFFFFu, upto, 31), gridDim.x);
+        const uint32_t first = ranges.first(blockIdx.x), last = ranges.first(blockIdx.x + 1);
+        count = (int)(last - first);
+        uint32_t at = upto - mine;
+        const bool holds = mine > 0 && at <= first && first < upto;     // one lane, if there are tiles at all
+        const bool joins = warp == 0 && blockIdx.y == 0;
+        start = Cursor{0, 0, 1, 0};
+        if (joins && p.sequences > (int)gridDim.x && lane == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+        __syncwarp();
+#pragma unroll
+        for (int n = 0; n < kWarpSchedule / 32; ++n) {
+            if (n < per && b0 + n < p.sequences) {
+                const int tiles = tiles_of(lens[n], p.plan.tile_shift);
+                if (at <= first && first < at + tiles) start = Cursor{b0 + n, (int)(first - at), tiles, lens[n]};
+                if (joins && at >= first && at < last) write_join(p, ranges, b0 + n, at, tiles);
+                at += tiles;
+            }
+        }
+        const int from = __ffs(__ballot_sync(0xFFFFFFFFu, holds)) - 1;
+        start.b = __shfl_sync(0xFFFFFFFFu, start.b, from & 31);
+        start.tile = __shfl_sync(0xFFFFFFFFu, start.tile, from & 31);
+        start.tiles = __shfl_sync(0xFFFFFFFFu, start.tiles, from & 31);
+        start.len = __shfl_sync(0xFFFFFFFFu, start.len, from & 31);
+        __syncthreads();                                                // the barriers are set up
+    } else {
+        const int per = (p.sequences + kThreads - 1) / kThreads;
+        const int b0 = min(p.sequences, tid * per), b1 = min(p.sequences, b0 + per);
+        uint32_t mine = 0;
+        bool wrong = false;
+#pragma unroll 4
+        for (int b = b0; b < b1; ++b) {
+            const int len = __ldg(p.seq_lens + b);
+            wrong |= len < 0 || len > p.capacity;
+            mine += tiles_of(min(max(len, 0), p.capacity), p.plan.tile_shift);
+        }
+        if (wrong && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
+        uint32_t upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
             if (lane >= off) upto += v;
         }
         if (lane == 31) warp_sums[warp] = upto;
+        if (blockIdx.y == 0 && p.sequences > (int)gridDim.x && tid == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
         __syncthreads();
-        int64_t total = 0;
+        uint32_t total = 0;
 #pragma unroll
-        for (int w = 0; w <= kWarps; ++w) {
+        for (int w = 0; w < kWarps + kProducers; ++w) {
             if (w == warp) upto += total;
             total += warp_sums[w];
         }
-        const int64_t ranges = min((int64_t)gridDim.x, (total + p.min_tiles - 1) / p.min_tiles);
-        const int64_t x = blockIdx.x;
-        const int64_t first = x < ranges ? x * total / ranges : total;
-        const int64_t last = x < ranges ? (x + 1) * total / ranges : total;
+        const Ranges ranges = ranges_of(total, gridDim.x);
+        const uint32_t first = ranges.first(blockIdx.x), last = ranges.first(blockIdx.x + 1);
         count = (int)(last - first);
-        // the threads whose sequences hold the first tile of a range, or
-        // start in it, write down what the joining kernel needs
-        int64_t at = upto - mine;
-        const bool by_sequence = p.sequences <= (int)gridDim.x;
-        if (blockIdx.y == 0 && !by_sequence) {
-            if (tid == 0) p.joins[x] = make_int4(0, 0, 0, 0);
-            __syncthreads();
-        }
+        uint32_t at = upto - mine;
+        if (at < last && upto > first) {
 #pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const int len = length_of(p, b), n = tiles_of(len, p.plan.tile_shift);
-            if (at <= first && first < at + n && count > 0) {
-                start_sh.b = b;
-                start_sh.tile = (int)(first - at);
-                start_sh.tiles = n;
-                start_sh.len = len;
+            for (int b = b0; b < b1; ++b) {
+                const int len = length_of(p, b), tiles = tiles_of(len, p.plan.tile_shift);
+                if (at <= first && first < at + tiles) start_sh = Cursor{b, (int)(first - at), tiles, len};
+                if (blockIdx.y == 0 && at >= first && at < last) write_join(p, ranges, b, at, tiles);
+                at += tiles;
             }
-            if (blockIdx.y == 0 && at >= first && at < last) {
-                const int64_t end = ((at + n) * ranges - 1) / total;      // range of the sequence's last tile
-                const int pieces = (int)(end - x) + 1;
-                if (by_sequence) p.joins[b] = make_int4(b, (int)x, pieces, 0);
-                else if (pieces > 1) p.joins[x] = make_int4(b, (int)x, pieces, 0);
-            }
-            at += n;
         }
         __syncthreads();
-        if (count <= 0) return;
+        start = start_sh;
     }
+    if (count <= 0) return;
 
     const PagedPlan &plan = p.plan;
     const int heads_cta = 1 << plan.heads_shift, tw = 1 << plan.parts_shift;
@@ -317,19 +399,21 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     const uint32_t v_scales = k_scales + tw * scale_groups * (16 * kTile);
     bool failed = false;
 
-    if (warp == kWarps) {
+    if (warp >= kWarps) {
         // ================= brings the tiles in =================
-        Cursor at = start_sh;
+        Cursor at = start;
         int left = count, stage = 0;
         uint32_t phase = 1;                                             // of `empty`: the first round passes
         auto acquire = [&]() {
-            if (!failed && !mbar_wait(&empty[stage], phase, p.timeout)) {
-                failed = true;
-                if (lane == 0) set_status(p.status, ST_TIMEOUT);
+            if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], phase))) {
+                failed = !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase, p.timeout));
+                if (failed && lane == 0) set_status(p.status, ST_TIMEOUT);
             }
-            failed = __any_sync(0xFFFFFFFFu, failed);
         };
+        int turn = warp - kWarps;                                       // tiles until this warp's next one
+        auto my_turn = [&]() { return turn == 0; };
         auto advance = [&]() {
+            turn = turn == 0 ? kProducers - 1 : turn - 1;
             if (++stage == plan.stages) {
                 stage = 0;
                 phase ^= 1u;
@@ -338,8 +422,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         if (p.tma) {
             // Lane l looks up 16 tokens: part l % tw of tile l / tw of a batch
             // of tiles of one sequence; the next batch is looked up before
-            // this one is copied.
+            // this one is copied.  One lane issues all copies of a stage (a
+            // TMA instruction takes its operands from one thread at a time).
             const int per_batch = 32 >> plan.parts_shift, my_part = lane & (tw - 1);
+            const int group_first = (head_first * S::kScales) >> 4;
+            const uint32_t part_codes = heads_cta * kTile * S::kCodes, part_scales = scale_groups * 16 * kTile;
             struct Batch {
                 int n, page, offset, tokens;
             };
@@ -360,8 +447,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 }
                 return f;
             };
-            const int group_first = (head_first * S::kScales) >> 4;
-            const uint32_t bytes = 2u * (heads_cta * kTile * S::kCodes + scale_groups * 16 * kTile);
+            const uint32_t bytes = 2u * (part_codes + part_scales);
             Batch f = lookup();
             while (f.n > 0) {
                 const Batch next = lookup();
@@ -372,26 +458,31 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 const int row = f.page * p.page_size + f.offset;
 #pragma unroll 1
                 for (int i = 0; i < f.n; ++i) {
-                    const int src = (i << plan.parts_shift) + my_part;
-                    const int r = __shfl_sync(0xFFFFFFFFu, row, src);
-                    const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, src);
+                    if (!my_turn()) {
+                        advance();
+                        continue;
+                    }
+                    const int from = (i << plan.parts_shift) + my_part;
+                    const int my_row = __shfl_sync(0xFFFFFFFFu, row, from);
+                    const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, from);
+                    const uint32_t there = __ballot_sync(0xFFFFFFFFu, lane < tw && tokens > 0);
                     acquire();
                     if (failed) break;
-                    const bool mine = lane < tw && tokens > 0;
                     if (lane < tw) masks[stage][lane] = (1 << tokens) - 1;
-                    const int parts = __popc(__ballot_sync(0xFFFFFFFFu, mine));
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], parts * bytes);
-                    __syncwarp();
-                    if (mine) {
-                        const uint32_t to = ring + stage * plan.stage_bytes;
-                        const uint32_t codes = to + lane * (heads_cta * kTile * S::kCodes);
-                        const uint32_t scales = to + lane * (scale_groups * 16 * kTile);
-                        tma_load_3d(codes, &maps.kc, &full[stage], 0, r, head_first);
-                        tma_load_3d(scales + k_scales, &maps.ks, &full[stage], 0, r, group_first);
-                        tma_load_3d(codes + v_codes, &maps.vc, &full[stage], 0, r, head_first);
-                        tma_load_3d(scales + v_scales, &maps.vs, &full[stage], 0, r, group_first);
+                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(there) * bytes);
+                    uint32_t to = ring + stage * plan.stage_bytes, scales = to + k_scales;
+#pragma unroll 1
+                    for (int n = 0; n < tw; ++n, to += part_codes, scales += part_scales) {
+                        const int r = __shfl_sync(0xFFFFFFFFu, my_row, n);
+                        if (lane == 0 && ((there >> n) & 1u)) {
+                            tma_load_3d(to, &maps.kc, &full[stage], 0, r, head_first);
+                            tma_load_3d(scales, &maps.ks, &full[stage], 0, r, group_first);
+                            tma_load_3d(to + v_codes, &maps.vc, &full[stage], 0, r, head_first);
+                            tma_load_3d(scales + (v_scales - k_scales), &maps.vs, &full[stage], 0, r, group_first);
+                        }
                     }
+                    __syncwarp();
                     advance();
                 }
                 if (failed) break;
@@ -403,6 +494,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             // and copied in 16-byte pieces of the codes and kScales of a
             // head's scales.
             const int tokens_stage = kTile << plan.parts_shift;
+            int *rows = rows_sh[warp - kWarps];
             const int piece_shift = plan.heads_shift + (kD == 64 ? 1 : kD == 128 ? 2 : 3);
             const int scales_from = (head_first * S::kScales) & ~15;
             int pages[4], offsets[4];                                   // tokens lane, lane + 32, ...
@@ -418,10 +510,18 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         pages[k] = __ldg(p.block_table + (int64_t)at.b * p.table_stride + entry);
                     }
                 }
-                if (left > 0) at.skip(p, 1, --left > 0);
             };
+            auto pass = [&](int n) {                                    // n tiles on
+                for (; n > 0 && left > 0; --n) at.skip(p, 1, --left > 0);
+            };
+            pass(turn);
             lookup();
+#pragma unroll 1
             for (int i = 0; i < count; ++i) {
+                if (!my_turn()) {
+                    advance();
+                    continue;
+                }
                 acquire();
                 if (failed) break;
 #pragma unroll
@@ -434,10 +534,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     const uint32_t mask = __ballot_sync(0xFFFFFFFFu, ok);
                     const int local = 32 * k + lane;
                     if (local < tokens_stage) {
-                        rows_sh[local] = ok ? pages[k] * p.page_size + offsets[k] : -1;
+                        rows[local] = ok ? pages[k] * p.page_size + offsets[k] : -1;
                         if ((lane & 15) == 0) masks[stage][local >> 4] = (int)((mask >> (lane & 16)) & 0xFFFFu);
                     }
                 }
+                pass(kProducers);
                 lookup();
                 __syncwarp();
                 const uint32_t to = ring + stage * plan.stage_bytes;
@@ -445,7 +546,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 for (int n = lane; n < tokens_stage << piece_shift; n += 32) {
                     const int t = n >> piece_shift, x = n & ((1 << piece_shift) - 1);
                     const int h = x / S::kChunks, ch = x % S::kChunks;
-                    const int r = rows_sh[t];
+                    const int r = rows[t];
                     if (r >= 0) {
                         const int64_t src = (int64_t)r * p.row_codes + (int64_t)(head_first + h) * S::kCodes + 16 * ch;
                         const uint32_t dst = to + (((t >> 4) << plan.heads_shift) + h) * (kTile * S::kCodes) +
@@ -457,7 +558,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll 2
                 for (int n = lane; n < tokens_stage << plan.heads_shift; n += 32) {
                     const int t = n >> plan.heads_shift, h = n & (heads_cta - 1);
-                    const int r = rows_sh[t];
+                    const int r = rows[t];
                     if (r >= 0) {
                         const int x = (head_first + h) * S::kScales;    // byte of the row
                         const int64_t src = (int64_t)r * p.row_scales + x;
@@ -494,7 +595,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     const int unit = hk * plan.units_head + sub;
     const int head0 = hk * p.group + sub * 8;
     const int heads = min(8, p.group - sub * 8);                        // query heads of this unit
-    const float cscale = __fdiv_rn(__fmul_rn(p.scale, kLog2e), *p.gk);
+    const float cscale = __fdiv_rn(__fmul_rn(p.scale, kLog2e), gk);
 
     // ---- lane constants of the fragment reads, from the start of a stage
     const int tk = token_of<kD>(g >> 1, g & 1);                         // token of MMA row g (row g + 8: + 8)
@@ -529,8 +630,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     uint32_t qb[2 * S::kSteps];          // B fragments of the query
     float oacc[S::kSteps][4];
     float lsum[2], mp[2], ck[2];
-    int b = start_sh.b, in_seq = start_sh.tiles - start_sh.tile;        // tiles to the end of the sequence
-    bool starts_here = start_sh.tile == 0;
+    int b = start.b, in_seq = start.tiles - start.tile;        // tiles to the end of the sequence
+    bool starts_here = start.tile == 0;
     int left = count, stage = 0;
     uint32_t phase = 0;
     const uint8_t *ring_at = smem_raw + (ring - smem_u32(smem_raw)), *at = ring_at;
@@ -582,13 +683,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         for (int tile = n_tiles; tile > 0; --tile) {
             // A wait that gives up leaves the CTA in step: its tiles then
             // count as empty, every barrier is still met.
-            if (!failed && !mbar_wait(&full[stage], phase, p.timeout)) {
-                failed = true;
-                set_status(p.status, ST_TIMEOUT);
+            if (!failed && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&full[stage], phase))) {
+                failed = !__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, p.timeout));
+                if (failed) set_status(p.status, ST_TIMEOUT);
             }
-            failed = __any_sync(0xFFFFFFFFu, failed);
             const uint32_t mask = failed ? 0u : (uint32_t)masks[stage][part];
-            if (mask != 0u) {
+
             // ---- S = K q^T
             float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -707,7 +807,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_f16(oacc[4 * n + k], even[0][k], odd[0][k], even[1][k], odd[1][k], p0, p1);
             }
-            }
             warp_sync();
             if (lane == 0) mbar_arrive(&empty[stage]);
             at += plan.stage_bytes;
@@ -718,80 +817,97 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             }
         }
 
-        // ---- end of this CTA's part of the sequence: join the unit's warps.
-        // Rolled loops through shared memory: this runs once a sequence, and
-        // straight-line code of it (130 KB with the loop above) cost more in
-        // instruction fetches than the work itself.
+        // ---- end of this CTA's part of the sequence: the unit's warps meet
+        // in shared memory, and each sums and stores its share of the M-tiles.
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) lsum[n] += __shfl_xor_sync(0xFFFFFFFFu, lsum[n], off);
-        if (g == 0) {
-            ml[warp][2 * c] = make_float2(mp[0], lsum[0]);
-            ml[warp][2 * c + 1] = make_float2(mp[1], lsum[1]);
+        if (tw > 1) {
+            if (g == 0) {
+                ml[warp][2 * c] = make_float2(mp[0], lsum[0]);
+                ml[warp][2 * c + 1] = make_float2(mp[1], lsum[1]);
+            }
+            unit_barrier(1 + unit_cta, 32 * tw);
         }
-        const int step = kWarps >> plan.parts_shift;                    // warps between two parts of a unit
-        auto unit_sync = [&]() {
-            if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
-            else warp_sync();
-        };
-        unit_sync();
-        float M[2] = {mp[0], mp[1]}, L[2] = {0.0f, 0.0f};
-#pragma unroll 1
-        for (int w = unit_cta; w < kWarps; w += step) {
-            M[0] = fmaxf(M[0], ml[w][2 * c].x);
-            M[1] = fmaxf(M[1], ml[w][2 * c + 1].x);
-        }
-#pragma unroll 1
-        for (int w = unit_cta; w < kWarps; w += step) {
-            const float2 v0 = ml[w][2 * c], v1 = ml[w][2 * c + 1];
-            L[0] += v0.y * exp2_fast(v0.x - M[0]);
-            L[1] += v1.y * exp2_fast(v1.x - M[1]);
-        }
-        {
-            const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
-            float *mine = sums + warp * (8 * kD) + lane;
-#pragma unroll
-            for (int j = 0; j < S::kSteps; ++j)
-#pragma unroll
-                for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
-        }
-        unit_sync();
         const bool whole = ends && starts_here;
+        uint16_t *o = p.o + (int64_t)b * p.os_b + (int64_t)(head0 + 2 * c) * p.os_h + (kD / 8) * g;
         const int64_t slot = (int64_t)(2 * blockIdx.x + (starts_here ? 1 : 0)) * plan.units + unit;
-        float f[2];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) f[n] = whole ? (L[n] == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(L[n], *p.gv))) : 1.0f;
-        uint16_t *o = p.o + (int64_t)b * p.os_b + (int64_t)head0 * p.os_h + (kD / 8) * g;
         float *part_o = p.part_o + slot * (8 * kD) + lane;
-#pragma unroll 1
-        for (int j = part; j < S::kSteps; j += tw) {
-            const float *from = sums + unit_cta * (8 * kD) + 128 * j + lane;
-            float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-            for (int w = 0; w < tw; ++w, from += step * (8 * kD)) {
+        auto finish = [&](auto parts) {
+            constexpr int kParts = decltype(parts)::value, kStep = kWarps / kParts;
+            if (kParts > 1) {
+                float M[2] = {mp[0], mp[1]}, L[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int n = 0; n < 4; ++n) r[n] += from[32 * n];
+                for (int w = 0; w < kParts; ++w) {
+                    M[0] = fmaxf(M[0], ml[unit_cta + w * kStep][2 * c].x);
+                    M[1] = fmaxf(M[1], ml[unit_cta + w * kStep][2 * c + 1].x);
+                }
+#pragma unroll
+                for (int w = 0; w < kParts; ++w) {
+                    const float2 v0 = ml[unit_cta + w * kStep][2 * c], v1 = ml[unit_cta + w * kStep][2 * c + 1];
+                    L[0] += v0.y * exp2_fast(v0.x - M[0]);
+                    L[1] += v1.y * exp2_fast(v1.x - M[1]);
+                }
+                const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
+                float *mine = sums + warp * (8 * kD) + lane;
+#pragma unroll
+                for (int j = 0; j < S::kSteps; ++j)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mp[n] = M[n];
+                    lsum[n] = L[n];
+                }
+                unit_barrier(1 + unit_cta, 32 * kParts);
             }
+            float f[2] = {1.0f, 1.0f};
             if (whole) {
+                const float gv = __ldg(p.gv);
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
-                    if (2 * c + n < heads)
-                        *reinterpret_cast<uint32_t *>(o + (int64_t)(2 * c + n) * p.os_h + 2 * j) =
-                            bf16x2_from_f32(r[n] * f[n], r[n + 2] * f[n]);
-            } else {
-#pragma unroll
-                for (int n = 0; n < 4; ++n) part_o[128 * j + 32 * n] = r[n];
+                for (int n = 0; n < 2; ++n) f[n] = lsum[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(lsum[n], gv));
             }
-        }
+            constexpr int kTiles = S::kSteps / kParts > 0 ? S::kSteps / kParts : 1;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                const int j = kParts == 1 ? i : part * kTiles + i;
+                if (kParts > S::kSteps && j >= S::kSteps) break;
+                float r[4];
+                if (kParts == 1) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) r[n] = oacc[i][n];
+                } else {
+                    const float *from = sums + unit_cta * (8 * kD) + 128 * j + lane;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) r[n] = from[32 * n];
+#pragma unroll
+                    for (int w = 1; w < kParts; ++w)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) r[n] += from[w * kStep * (8 * kD) + 32 * n];
+                }
+                if (whole) {
+                    if (2 * c < heads)
+                        *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0], r[2] * f[0]);
+                    if (2 * c + 1 < heads)
+                        *reinterpret_cast<uint32_t *>(o + p.os_h + 2 * j) = bf16x2_from_f32(r[1] * f[1], r[3] * f[1]);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) part_o[128 * j + 32 * n] = r[n];
+                }
+            }
+        };
+        if (plan.parts_shift == 0) finish(Parts<1>{});
+        else if (plan.parts_shift == 1) finish(Parts<2>{});
+        else if (plan.parts_shift == 2) finish(Parts<4>{});
+        else finish(Parts<8>{});
         if (part == 0 && g == 0) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 if (!whole)
-                    p.part_ml[slot * 8 + 2 * c + n] = make_float2(M[n], L[n]);
+                    p.part_ml[slot * 8 + 2 * c + n] = make_float2(mp[n], lsum[n]);
                 else if (p.lse != nullptr && 2 * c + n < heads)
-                    p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] =
-                        L[n] == 0.0f ? -__int_as_float(0x7F800000) : (M[n] + log2f(L[n])) * kLn2;
+                    p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] = lse_of(mp[n], lsum[n]);
             }
         }
         // The next sequence's sums are written only after every warp of the
@@ -807,11 +923,9 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 // (or the range at whose end one is cut); its items are the M-tiles of O^T of
 // each unit (128 values: 8 heads x 16 dims).  A warp takes four parts in one
 // round of loads -- their maxima, sums and values -- with the running maximum
-// and sum of the online softmax.  A sequence of few parts gets a warp an
-// item; one of many a CTA an item, whose warps deal the parts among them and
-// are joined in shared memory.
+// and sum of the online softmax; 1 to 16 warps take an item by the number of
+// its parts, and are joined in shared memory.
 constexpr int kJoinWarps = 16;
-constexpr int kFewParts = 16;
 
 struct JoinState {
     float m, l;          // of head lane % 8
@@ -870,11 +984,11 @@ __device__ __forceinline__ void join_store(const PagedAttnParams &p, int dim, in
     const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
     const int head0 = hk * p.group + sub * 8;
     if (h >= min(8, p.group - sub * 8)) return;
-    const float f = L == 0.0f ? 0.0f : __fdiv_rn(1.0f, __fmul_rn(L, *p.gv));
+    const float f = L == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(L, __ldg(p.gv)));
     *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + h) * p.os_h + (dim / 8) * g + 2 * j) =
         bf16x2_from_f32(lo * f, hi * f);
     if (j == 0 && g == 0 && p.lse != nullptr)
-        p.lse[(int64_t)b * p.heads_q + head0 + h] = L == 0.0f ? -__int_as_float(0x7F800000) : (M + log2f(L)) * kLn2;
+        p.lse[(int64_t)b * p.heads_q + head0 + h] = lse_of(M, L);
 }
 
 __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_constant__ PagedAttnParams p, int dim) {
@@ -885,46 +999,37 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_
     const int4 join = p.joins[blockIdx.x];
     const int b = join.x, x0 = join.y, pieces = join.z;
     if (pieces <= 1) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tiles = dim / 16, items = p.plan.units * tiles;
-    if (pieces <= kFewParts) {
+    // log2 of the warps an item: enough for one round, or for two where that
+    // would leave items for another pass
+    int shift = 0;
+    while (shift < 4 && (4 << shift) < pieces) ++shift;
+    if (shift > 0 && (int)gridDim.y * (kJoinWarps >> shift) < items) --shift;
+    const int mine = warp & ((1 << shift) - 1), first = warp - mine;    // place in the item's warps; the first of them
 #pragma unroll 1
-        for (int item = blockIdx.y * kJoinWarps + warp; item < items; item += gridDim.y * kJoinWarps) {
-            const int unit = item / tiles, j = item - unit * tiles;
-            const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 0, 4, lane);
-            // lane 8 n + 4 k + ...: value n of lane rows and heads; n and n + 2 meet
-            __syncwarp();
+    for (int at = blockIdx.y * (kJoinWarps >> shift); at < items; at += gridDim.y * (kJoinWarps >> shift)) {
+        const int item = at + (warp >> shift);
+        const int unit = item / tiles, j = item - unit * tiles;
+        if (item < items) {
+            const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 4 * mine, 4 << shift, lane);
             *reinterpret_cast<float4 *>(&sums[warp][4 * lane]) = s.a;
             if (lane < 8) ml[warp][lane] = make_float2(s.m, s.l);
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int h = lane & 7, g = (lane >> 3) + 4 * k, at = (h & 1) * 32 + g * 4 + (h >> 1);
-                join_store(p, dim, b, unit, j, h, g, ml[warp][h].x, ml[warp][h].y, sums[warp][at], sums[warp][at + 64]);
-            }
         }
-        return;
-    }
-#pragma unroll 1
-    for (int item = blockIdx.y; item < items; item += gridDim.y) {
-        const int unit = item / tiles, j = item - unit * tiles;
-        const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 4 * warp, 4 * kJoinWarps, lane);
-        *reinterpret_cast<float4 *>(&sums[warp][4 * lane]) = s.a;
-        if (lane < 8) ml[warp][lane] = make_float2(s.m, s.l);
         __syncthreads();
-        if (tid < 64) {
-            const int h = tid & 7, g = tid >> 3, at = (h & 1) * 32 + g * 4 + (h >> 1);
-            float M = kLowest, L = 0.0f, lo = 0.0f, hi = 0.0f;
-#pragma unroll
-            for (int n = 0; n < kJoinWarps; ++n) M = fmaxf(M, ml[n][h].x);
-#pragma unroll
-            for (int n = 0; n < kJoinWarps; ++n) {
-                const float w = exp2_fast(ml[n][h].x - M);
-                L += w * ml[n][h].y;
-                lo += w * sums[n][at];
-                hi += w * sums[n][at + 64];
+        if (item < items) {
+            for (int n = 32 * mine + lane; n < 64; n += 32 << shift) {
+                const int h = n & 7, g = n >> 3, from = (h & 1) * 32 + g * 4 + (h >> 1);
+                float M = kLowest, L = 0.0f, lo = 0.0f, hi = 0.0f;
+                for (int w = first; w < first + (1 << shift); ++w) M = fmaxf(M, ml[w][h].x);
+                for (int w = first; w < first + (1 << shift); ++w) {
+                    const float f = exp2_fast(ml[w][h].x - M);
+                    L += f * ml[w][h].y;
+                    lo += f * sums[w][from];
+                    hi += f * sums[w][from + 64];
+                }
+                join_store(p, dim, b, unit, j, h, g, M, L, lo, hi);
             }
-            join_store(p, dim, b, unit, j, h, g, M, L, lo, hi);
         }
         __syncthreads();
     }
@@ -972,10 +1077,10 @@ cudaError_t launch_paged_attention(const PagedAttnParams &p, const PagedMaps &ma
                                  : launch_main<256>(p, maps, s);
     if (e != cudaSuccess) return e;
     // the sequences that can be cut; CTAs for a warp an item, and where the
-    // sequences are few, up to a CTA an item, within about two an SM
+    // sequences are few, up to a CTA an item, within about four an SM
     const int joins = std::min(p.sequences, p.plan.ranges);
     const int items = p.plan.units * (dim / 16);
-    const int y = std::min(items, std::max((items + kJoinWarps - 1) / kJoinWarps, 296 / joins));
+    const int y = std::min(items, std::max((items + kJoinWarps - 1) / kJoinWarps, 592 / joins));
     void *args[] = {const_cast<PagedAttnParams *>(&p), &dim};
     return launch_dependent((const void *)k_paged_combine, dim3((unsigned)joins, (unsigned)y), 32 * kJoinWarps, 0, s, args);
 }

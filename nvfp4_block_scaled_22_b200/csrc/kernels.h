@@ -286,7 +286,6 @@ __global__ void k_kv_read(KvReadParams p);
 // the tile of 16 x parts tokens that a stage of the ring holds.
 constexpr int kPagedMaxRanges = 296;
 constexpr int kPagedMaxStages = 8;
-constexpr int kPagedMinTiles = 1;
 constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
 constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
 #ifndef PU
@@ -328,7 +327,7 @@ inline size_t paged_scratch_bytes(const PagedPlan &n, int dim) {
 // Codes as (byte of a head, row, head), boxes of one head's bytes x 16 rows x
 // the CTA's heads; scales as (byte of 16, row, group of 16 bytes).
 struct PagedMaps {
-    CUtensorMap kc, ks, vc, vs;
+    CUtensorMap kc, ks, vc, vs;      // in this order: indexed from the first
 };
 
 struct PagedAttnParams {
@@ -346,7 +345,6 @@ struct PagedAttnParams {
     FastDiv page_div;
     PagedPlan plan;
     int32_t tma;             // page_size % 16 == 0 (16 tokens share a page) and 16-byte scale rows: tiles by TMA
-    int32_t min_tiles;       // tiles a range has at least (but the last)
     long long timeout;       // clock bound of a wait
     float scale;
     uint16_t *o;
