@@ -1073,6 +1073,7 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     p.page_size = page_size;
     p.page_div = fast_div((uint32_t)page_size);
     p.plan = plan;
+    p.sub_blocks = fast_div((uint32_t)(plan.units_head >> plan.subs_shift));
     p.tma = page_size % 16 == 0 && p.row_scales % 16 == 0 && K->rows > 0;
     p.timeout = g_timeout_cycles;
     p.scale = scale;
@@ -1083,8 +1084,8 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     p.status = static_cast<uint32_t *>(workspace);
     const int64_t parts = (int64_t)2 * plan.ranges * plan.units;
     p.joins = static_cast<int4 *>(scratch);
-    p.part_o = reinterpret_cast<float *>(p.joins + plan.ranges);
-    p.part_ml = reinterpret_cast<float2 *>(p.part_o + parts * 8 * dim);
+    p.part_o = reinterpret_cast<float4 *>(p.joins + plan.ranges);
+    p.part_ml = p.part_o + parts * 2 * dim;
     PagedMaps maps = {};
     if (p.tma) {
         st = get_encode();

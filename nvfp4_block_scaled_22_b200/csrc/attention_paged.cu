@@ -61,10 +61,7 @@ constexpr float kOffset = 6.0f;      // m' is this much below the reference
 constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' moves
 
 constexpr int kWarps = 8;            // warps that compute
-#ifndef NP
-#define NP 2
-#endif
-constexpr int kProducers = NP;       // warps that bring the tiles in, stages in turn
+constexpr int kProducers = 2;       // warps that bring the tiles in, stages in turn
 constexpr int kThreads = 32 * (kWarps + kProducers);
 constexpr int kTile = 16;            // tokens of a warp's tile
 
@@ -161,11 +158,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return d;
 }
 
-template <int kN>
-struct Parts {
-    static constexpr int value = kN;
-};
-
 // log of a sum l of 2^(x - m), natural; lg2.approx is off by at most 2^-22
 // (l is 0 or at least 1)
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -244,7 +236,7 @@ __device__ __forceinline__ Ranges ranges_of(uint32_t total, uint32_t ctas) {
     return r;
 }
 
-constexpr int kWarpSchedule = 128;   // up to this many sequences each warp works the schedule out for itself
+constexpr int kWarpSchedule = 32;   // up to this many sequences each warp works the schedule out for itself
 
 // What the joining kernel has to know of a sequence that starts in this range.
 __device__ __forceinline__ void write_join(const PagedAttnParams &p, const Ranges &r, int b, uint32_t at, int tiles) {
@@ -257,20 +249,21 @@ __device__ __forceinline__ void write_join(const PagedAttnParams &p, const Range
 struct Cursor {
     int b, tile, tiles, len;
     // n tiles on, n at most to the end of the sequence
+    template <int kTileShift>
     __device__ __forceinline__ void skip(const PagedAttnParams &p, int n, bool more) {
         tile += n;
         if (tile == tiles) {
             ++b;
             tile = 0;
             len = more ? length_of(p, b) : 0;
-            tiles = tiles_of(len, p.plan.tile_shift);
+            tiles = tiles_of(len, kTileShift);
         }
     }
 };
 
 }  // namespace
 
-template <int kD>
+template <int kD, bool kTma, int kPartsShift>
 __global__ void __launch_bounds__(kThreads, Shape<kD>::kCtasPerSm)
 k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_constant__ PagedMaps maps) {
     using S = Shape<kD>;
@@ -278,13 +271,13 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
     __shared__ int masks[kPagedMaxStages][kWarps];
     __shared__ int rows_sh[kProducers][kWarps * kTile];  // pool rows of a stage's tokens (copies without TMA)
-    __shared__ float2 ml[kWarps][8];
+    __shared__ float4 ml[kWarps][4];                     // (m, l) of heads 2c and 2c + 1
     __shared__ uint32_t warp_sums[kWarps + kProducers];
     __shared__ Cursor start_sh;
     grid_dependents_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid < p.plan.stages) {
-        mbar_init(&full[tid], p.tma ? 1 : 33);
+        mbar_init(&full[tid], kTma ? 1 : 33);
         mbar_init(&empty[tid], kWarps);
     }
     fence_barrier_init();
@@ -309,7 +302,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 const int len = __ldg(p.seq_lens + b0 + n);
                 wrong |= len < 0 || len > p.capacity;
                 lens[n] = min(max(len, 0), p.capacity);
-                mine += tiles_of(lens[n], p.plan.tile_shift);
+                mine += tiles_of(lens[n], (4 + kPartsShift));
             }
         }
         if (wrong && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
@@ -331,7 +324,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
         for (int n = 0; n < kWarpSchedule / 32; ++n) {
             if (n < per && b0 + n < p.sequences) {
-                const int tiles = tiles_of(lens[n], p.plan.tile_shift);
+                const int tiles = tiles_of(lens[n], (4 + kPartsShift));
                 if (at <= first && first < at + tiles) start = Cursor{b0 + n, (int)(first - at), tiles, lens[n]};
                 if (joins && at >= first && at < last) write_join(p, ranges, b0 + n, at, tiles);
                 at += tiles;
@@ -352,7 +345,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         for (int b = b0; b < b1; ++b) {
             const int len = __ldg(p.seq_lens + b);
             wrong |= len < 0 || len > p.capacity;
-            mine += tiles_of(min(max(len, 0), p.capacity), p.plan.tile_shift);
+            mine += tiles_of(min(max(len, 0), p.capacity), (4 + kPartsShift));
         }
         if (wrong && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
         uint32_t upto = mine;
@@ -377,7 +370,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         if (at < last && upto > first) {
 #pragma unroll 1
             for (int b = b0; b < b1; ++b) {
-                const int len = length_of(p, b), tiles = tiles_of(len, p.plan.tile_shift);
+                const int len = length_of(p, b), tiles = tiles_of(len, (4 + kPartsShift));
                 if (at <= first && first < at + tiles) start_sh = Cursor{b, (int)(first - at), tiles, len};
                 if (blockIdx.y == 0 && at >= first && at < last) write_join(p, ranges, b, at, tiles);
                 at += tiles;
@@ -389,9 +382,10 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     if (count <= 0) return;
 
     const PagedPlan &plan = p.plan;
-    const int heads_cta = 1 << plan.heads_shift, tw = 1 << plan.parts_shift;
-    const int sub_blocks = plan.units_head >> plan.subs_shift;          // CTAs over the units of a head
-    const int head_first = (int)(blockIdx.y / sub_blocks) << plan.heads_shift;
+    constexpr int tw = 1 << kPartsShift;                                // warps that share a unit's tokens
+    const int heads_cta = 1 << plan.heads_shift;
+    const int head_block = (int)quotient(blockIdx.y, p.sub_blocks);     // CTAs over the heads, then over a head's units
+    const int head_first = head_block << plan.heads_shift;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t v_codes = (uint32_t)(tw * heads_cta * kTile) * S::kCodes;   // within a stage: K codes, V codes, scales
     const uint32_t k_scales = 2 * v_codes;
@@ -419,12 +413,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 phase ^= 1u;
             }
         };
-        if (p.tma) {
+        if constexpr (kTma) {
             // Lane l looks up 16 tokens: part l % tw of tile l / tw of a batch
             // of tiles of one sequence; the next batch is looked up before
             // this one is copied.  One lane issues all copies of a stage (a
             // TMA instruction takes its operands from one thread at a time).
-            const int per_batch = 32 >> plan.parts_shift, my_part = lane & (tw - 1);
+            const int per_batch = 32 >> kPartsShift, my_part = lane & (tw - 1);
             const int group_first = (head_first * S::kScales) >> 4;
             const uint32_t part_codes = heads_cta * kTile * S::kCodes, part_scales = scale_groups * 16 * kTile;
             struct Batch {
@@ -434,8 +428,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 Batch f = {0, 0, 0, 0};
                 if (left > 0) {
                     f.n = min(per_batch, min(left, at.tiles - at.tile));
-                    const int my_tile = lane >> plan.parts_shift;
-                    const int t = ((at.tile + my_tile) << plan.tile_shift) + kTile * my_part;
+                    const int my_tile = lane >> kPartsShift;
+                    const int t = ((at.tile + my_tile) << (4 + kPartsShift)) + kTile * my_part;
                     if (my_tile < f.n && t < at.len) {
                         const uint32_t entry = quotient((uint32_t)t, p.page_div);
                         f.offset = t - (int)(entry * p.page_div.d);
@@ -443,7 +437,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         f.page = __ldg(p.block_table + (int64_t)at.b * p.table_stride + entry);
                     }
                     left -= f.n;
-                    at.skip(p, f.n, left > 0);
+                    at.skip<4 + kPartsShift>(p, f.n, left > 0);
                 }
                 return f;
             };
@@ -462,7 +456,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         advance();
                         continue;
                     }
-                    const int from = (i << plan.parts_shift) + my_part;
+                    const int from = (i << kPartsShift) + my_part;
                     const int my_row = __shfl_sync(0xFFFFFFFFu, row, from);
                     const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, from);
                     const uint32_t there = __ballot_sync(0xFFFFFFFFu, lane < tw && tokens > 0);
@@ -493,7 +487,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             // by: the rows of a stage's tokens are looked up one stage ahead,
             // and copied in 16-byte pieces of the codes and kScales of a
             // head's scales.
-            const int tokens_stage = kTile << plan.parts_shift;
+            const int tokens_stage = kTile << kPartsShift;
             int *rows = rows_sh[warp - kWarps];
             const int piece_shift = plan.heads_shift + (kD == 64 ? 1 : kD == 128 ? 2 : 3);
             const int scales_from = (head_first * S::kScales) & ~15;
@@ -503,7 +497,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 for (int k = 0; k < 4; ++k) {
                     pages[k] = -1;
                     offsets[k] = -1;
-                    const int local = 32 * k + lane, t = (at.tile << plan.tile_shift) + local;
+                    const int local = 32 * k + lane, t = (at.tile << (4 + kPartsShift)) + local;
                     if (left > 0 && local < tokens_stage && t < at.len) {
                         const uint32_t entry = quotient((uint32_t)t, p.page_div);
                         offsets[k] = t - (int)(entry * p.page_div.d);
@@ -512,7 +506,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 }
             };
             auto pass = [&](int n) {                                    // n tiles on
-                for (; n > 0 && left > 0; --n) at.skip(p, 1, --left > 0);
+                for (; n > 0 && left > 0; --n) at.skip<4 + kPartsShift>(p, 1, --left > 0);
             };
             pass(turn);
             lookup();
@@ -591,11 +585,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     const int part = warp >> (plan.heads_shift + plan.subs_shift);
     const int head_cta = unit_cta >> plan.subs_shift;
     const int hk = head_first + head_cta;
-    const int sub = (int)((blockIdx.y % sub_blocks) << plan.subs_shift) + (unit_cta & ((1 << plan.subs_shift) - 1));
+    const int sub = (((int)blockIdx.y - head_block * (int)p.sub_blocks.d) << plan.subs_shift) + (unit_cta & ((1 << plan.subs_shift) - 1));
     const int unit = hk * plan.units_head + sub;
     const int head0 = hk * p.group + sub * 8;
     const int heads = min(8, p.group - sub * 8);                        // query heads of this unit
-    const float cscale = __fdiv_rn(__fmul_rn(p.scale, kLog2e), gk);
+    const float cscale = __fmul_rn(__fmul_rn(p.scale, kLog2e), __frcp_rn(gk));
 
     // ---- lane constants of the fragment reads, from the start of a stage
     const int tk = token_of<kD>(g >> 1, g & 1);                         // token of MMA row g (row g + 8: + 8)
@@ -636,7 +630,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     uint32_t phase = 0;
     const uint8_t *ring_at = smem_raw + (ring - smem_u32(smem_raw)), *at = ring_at;
     // the warps' O, where several share a unit's tokens
-    float *sums = reinterpret_cast<float *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
+    float4 *sums = reinterpret_cast<float4 *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
 
     while (true) {
         {   // query of head g: lane c holds dims kD / 4 * c ... (kD = 256: 32c .. + 31 and 128 + 32c .. + 31)
@@ -819,102 +813,78 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 
         // ---- end of this CTA's part of the sequence: the unit's warps meet
         // in shared memory, and each sums and stores its share of the M-tiles.
+        // Compact on purpose: this code is cold when it is reached, and cold
+        // straight-line code costs some 40 cycles an instruction to fetch.
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) lsum[n] += __shfl_xor_sync(0xFFFFFFFFu, lsum[n], off);
-        if (tw > 1) {
-            if (g == 0) {
-                ml[warp][2 * c] = make_float2(mp[0], lsum[0]);
-                ml[warp][2 * c + 1] = make_float2(mp[1], lsum[1]);
-            }
-            unit_barrier(1 + unit_cta, 32 * tw);
+        float4 *mine = sums + warp * (2 * kD) + lane;
+#pragma unroll
+        for (int j = 0; j < S::kSteps; ++j) mine[32 * j] = make_float4(oacc[j][0], oacc[j][1], oacc[j][2], oacc[j][3]);
+        if (g == 0) ml[warp][c] = make_float4(mp[0], lsum[0], mp[1], lsum[1]);
+        const int step = kWarps >> kPartsShift;                    // warps between two parts of a unit
+        if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
+        else warp_sync();
+        float M[2] = {kLowest, kLowest}, L[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int w = unit_cta; w < kWarps; w += step) {
+            const float4 v = ml[w][c];
+            M[0] = fmaxf(M[0], v.x);
+            M[1] = fmaxf(M[1], v.z);
+        }
+#pragma unroll 1
+        for (int w = unit_cta; w < kWarps; w += step) {
+            const float4 v = ml[w][c];
+            L[0] += v.y * exp2_fast(v.x - M[0]);
+            L[1] += v.w * exp2_fast(v.z - M[1]);
         }
         const bool whole = ends && starts_here;
-        uint16_t *o = p.o + (int64_t)b * p.os_b + (int64_t)(head0 + 2 * c) * p.os_h + (kD / 8) * g;
+        float f[2] = {1.0f, 1.0f};
+        if (whole) {
+            const float gv = __ldg(p.gv);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) f[n] = L[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(L[n], gv));
+        }
+        const int h = head0 + 2 * c;
+        const bool h0 = 2 * c < heads, h1 = 2 * c + 1 < heads;
+        uint16_t *o = p.o + (int64_t)b * p.os_b + (int64_t)h * p.os_h + (kD / 8) * g;
         const int64_t slot = (int64_t)(2 * blockIdx.x + (starts_here ? 1 : 0)) * plan.units + unit;
-        float *part_o = p.part_o + slot * (8 * kD) + lane;
-        auto finish = [&](auto parts) {
-            constexpr int kParts = decltype(parts)::value, kStep = kWarps / kParts;
-            if (kParts > 1) {
-                float M[2] = {mp[0], mp[1]}, L[2] = {0.0f, 0.0f};
-#pragma unroll
-                for (int w = 0; w < kParts; ++w) {
-                    M[0] = fmaxf(M[0], ml[unit_cta + w * kStep][2 * c].x);
-                    M[1] = fmaxf(M[1], ml[unit_cta + w * kStep][2 * c + 1].x);
-                }
-#pragma unroll
-                for (int w = 0; w < kParts; ++w) {
-                    const float2 v0 = ml[unit_cta + w * kStep][2 * c], v1 = ml[unit_cta + w * kStep][2 * c + 1];
-                    L[0] += v0.y * exp2_fast(v0.x - M[0]);
-                    L[1] += v1.y * exp2_fast(v1.x - M[1]);
-                }
-                const float f0 = exp2_fast(mp[0] - M[0]), f1 = exp2_fast(mp[1] - M[1]);
-                float *mine = sums + warp * (8 * kD) + lane;
-#pragma unroll
-                for (int j = 0; j < S::kSteps; ++j)
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) mine[(4 * j + n) * 32] = oacc[j][n] * (n & 1 ? f1 : f0);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    mp[n] = M[n];
-                    lsum[n] = L[n];
-                }
-                unit_barrier(1 + unit_cta, 32 * kParts);
+        float4 *part_o = p.part_o + slot * (2 * kD) + lane;
+#pragma unroll 1
+        for (int j = part; j < S::kSteps; j += tw) {
+            float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+            for (int w = unit_cta; w < kWarps; w += step) {
+                const float4 v = sums[w * (2 * kD) + 32 * j + lane], x = ml[w][c];
+                const float f0 = exp2_fast(x.x - M[0]), f1 = exp2_fast(x.z - M[1]);
+                r[0] += v.x * f0;
+                r[1] += v.y * f1;
+                r[2] += v.z * f0;
+                r[3] += v.w * f1;
             }
-            float f[2] = {1.0f, 1.0f};
             if (whole) {
-                const float gv = __ldg(p.gv);
-#pragma unroll
-                for (int n = 0; n < 2; ++n) f[n] = lsum[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(lsum[n], gv));
-            }
-            constexpr int kTiles = S::kSteps / kParts > 0 ? S::kSteps / kParts : 1;
-#pragma unroll
-            for (int i = 0; i < kTiles; ++i) {
-                const int j = kParts == 1 ? i : part * kTiles + i;
-                if (kParts > S::kSteps && j >= S::kSteps) break;
-                float r[4];
-                if (kParts == 1) {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) r[n] = oacc[i][n];
-                } else {
-                    const float *from = sums + unit_cta * (8 * kD) + 128 * j + lane;
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) r[n] = from[32 * n];
-#pragma unroll
-                    for (int w = 1; w < kParts; ++w)
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) r[n] += from[w * kStep * (8 * kD) + 32 * n];
-                }
-                if (whole) {
-                    if (2 * c < heads)
-                        *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0], r[2] * f[0]);
-                    if (2 * c + 1 < heads)
-                        *reinterpret_cast<uint32_t *>(o + p.os_h + 2 * j) = bf16x2_from_f32(r[1] * f[1], r[3] * f[1]);
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n) part_o[128 * j + 32 * n] = r[n];
-                }
-            }
-        };
-        if (plan.parts_shift == 0) finish(Parts<1>{});
-        else if (plan.parts_shift == 1) finish(Parts<2>{});
-        else if (plan.parts_shift == 2) finish(Parts<4>{});
-        else finish(Parts<8>{});
-        if (part == 0 && g == 0) {
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                if (!whole)
-                    p.part_ml[slot * 8 + 2 * c + n] = make_float2(mp[n], lsum[n]);
-                else if (p.lse != nullptr && 2 * c + n < heads)
-                    p.lse[(int64_t)b * p.heads_q + head0 + 2 * c + n] = lse_of(mp[n], lsum[n]);
+                if (h0) *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0], r[2] * f[0]);
+                if (h1) *reinterpret_cast<uint32_t *>(o + p.os_h + 2 * j) = bf16x2_from_f32(r[1] * f[1], r[3] * f[1]);
+            } else {
+                part_o[32 * j] = make_float4(r[0], r[1], r[2], r[3]);
             }
         }
-        // The next sequence's sums are written only after every warp of the
-        // unit has met the first of the two barriers above again.
+        if (part == 0 && g == 0) {
+            if (!whole) {
+                p.part_ml[slot * 4 + c] = make_float4(M[0], L[0], M[1], L[1]);
+            } else if (p.lse != nullptr) {
+                float *lse = p.lse + (int64_t)b * p.heads_q + h;
+                if (h0) lse[0] = lse_of(M[0], L[0]);
+                if (h1) lse[1] = lse_of(M[1], L[1]);
+            }
+        }
+        // what is read above is written again only behind the next barrier of the unit
+        if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
+        else warp_sync();
         if (left == 0) break;
         ++b;
-        in_seq = tiles_of(length_of(p, b), plan.tile_shift);
+        in_seq = tiles_of(length_of(p, b), (4 + kPartsShift));
         starts_here = true;
     }
 }
@@ -927,80 +897,15 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 // its parts, and are joined in shared memory.
 constexpr int kJoinWarps = 16;
 
-struct JoinState {
-    float m, l;          // of head lane % 8
-    float4 a;            // values 4 lane .. + 3 of the M-tile
-};
-
-__device__ __forceinline__ JoinState join_parts(const PagedAttnParams &p, int dim, int x0, int pieces, int unit,
-                                                int j, int from, int step, int lane) {
-    // [n = 0 .. 3][lane of the MMA]: four neighbouring lanes are heads 0, 2,
-    // 4, 6 (n even) or 1, 3, 5, 7 (n odd)
-    const int odd = (lane >> 3) & 1, units = p.plan.units;
-    JoinState s = {kLowest, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
-    // piece n: the first lies in the second slot of its range, the others in the first
-    auto slot = [&](int n) { return (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit; };
-#pragma unroll 1
-    for (int n0 = from; n0 < pieces; n0 += step) {
-        float4 o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            o[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + slot(min(n0 + k, pieces - 1)) * (8 * dim) + 128 * j) + lane);
-        const int n = n0 + (lane >> 3);
-        float2 v = make_float2(kLowest, 0.0f);
-        if (n < pieces) v = __ldcg(p.part_ml + slot(n) * 8 + (lane & 7));
-        float top = fmaxf(s.m, v.x);
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 8));
-        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 16));
-        const float alpha = exp2_fast(s.m - top), w = n < pieces ? exp2_fast(v.x - top) : 0.0f;
-        s.m = top;
-        float wl = w * v.y;
-        wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 8);
-        wl += __shfl_xor_sync(0xFFFFFFFFu, wl, 16);
-        s.l = s.l * alpha + wl;
-        s.a.x *= __shfl_sync(0xFFFFFFFFu, alpha, odd);
-        s.a.y *= __shfl_sync(0xFFFFFFFFu, alpha, 2 + odd);
-        s.a.z *= __shfl_sync(0xFFFFFFFFu, alpha, 4 + odd);
-        s.a.w *= __shfl_sync(0xFFFFFFFFu, alpha, 6 + odd);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float w0 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + odd), w1 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 2 + odd);
-            const float w2 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 4 + odd), w3 = __shfl_sync(0xFFFFFFFFu, w, 8 * k + 6 + odd);
-            if (n0 + k < pieces) {
-                s.a.x += o[k].x * w0;
-                s.a.y += o[k].y * w1;
-                s.a.z += o[k].z * w2;
-                s.a.w += o[k].w * w3;
-            }
-        }
-    }
-    return s;
-}
-
-// Values n = e and n = e + 2 (dims 2j, 2j + 1 of lane row g) of head h = 2c + e,
-// summed as lo and hi with the weights' sum L under the maximum M.
-__device__ __forceinline__ void join_store(const PagedAttnParams &p, int dim, int b, int unit, int j, int h, int g,
-                                           float M, float L, float lo, float hi) {
-    const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
-    const int head0 = hk * p.group + sub * 8;
-    if (h >= min(8, p.group - sub * 8)) return;
-    const float f = L == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(L, __ldg(p.gv)));
-    *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(head0 + h) * p.os_h + (dim / 8) * g + 2 * j) =
-        bf16x2_from_f32(lo * f, hi * f);
-    if (j == 0 && g == 0 && p.lse != nullptr)
-        p.lse[(int64_t)b * p.heads_q + head0 + h] = lse_of(M, L);
-}
-
 __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_constant__ PagedAttnParams p, int dim) {
-    __shared__ float2 ml[kJoinWarps][8];
-    __shared__ float sums[kJoinWarps][128];
+    __shared__ float4 ml[kJoinWarps][4], sums[kJoinWarps][32];
     grid_dependents_launch();
     grid_dependency_wait();
     const int4 join = p.joins[blockIdx.x];
     const int b = join.x, x0 = join.y, pieces = join.z;
     if (pieces <= 1) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int tiles = dim / 16, items = p.plan.units * tiles;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    const int tiles = dim / 16, units = p.plan.units, items = units * tiles;
     // log2 of the warps an item: enough for one round, or for two where that
     // would leave items for another pass
     int shift = 0;
@@ -1011,27 +916,78 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_
     for (int at = blockIdx.y * (kJoinWarps >> shift); at < items; at += gridDim.y * (kJoinWarps >> shift)) {
         const int item = at + (warp >> shift);
         const int unit = item / tiles, j = item - unit * tiles;
-        if (item < items) {
-            const JoinState s = join_parts(p, dim, x0, pieces, unit, j, 4 * mine, 4 << shift, lane);
-            *reinterpret_cast<float4 *>(&sums[warp][4 * lane]) = s.a;
-            if (lane < 8) ml[warp][lane] = make_float2(s.m, s.l);
-        }
-        __syncthreads();
-        if (item < items) {
-            for (int n = 32 * mine + lane; n < 64; n += 32 << shift) {
-                const int h = n & 7, g = n >> 3, from = (h & 1) * 32 + g * 4 + (h >> 1);
-                float M = kLowest, L = 0.0f, lo = 0.0f, hi = 0.0f;
-                for (int w = first; w < first + (1 << shift); ++w) M = fmaxf(M, ml[w][h].x);
-                for (int w = first; w < first + (1 << shift); ++w) {
-                    const float f = exp2_fast(ml[w][h].x - M);
-                    L += f * ml[w][h].y;
-                    lo += f * sums[w][from];
-                    hi += f * sums[w][from + 64];
-                }
-                join_store(p, dim, b, unit, j, h, g, M, L, lo, hi);
+        // piece n: the first lies in the second slot of its range, the others in the first
+        auto slot = [&](int n) { return (int64_t)(2 * (x0 + n) + (n == 0 ? 1 : 0)) * units + unit; };
+        float m[2] = {kLowest, kLowest}, l[2] = {0.0f, 0.0f}, a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int n0 = 4 * mine; n0 < pieces && item < items; n0 += 4 << shift) {
+            float4 o[4], v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = min(n0 + k, pieces - 1);
+                o[k] = __ldcg(p.part_o + slot(n) * (2 * dim) + 32 * j + lane);
+                v[k] = __ldcg(p.part_ml + slot(n) * 4 + c);
+                if (n0 + k >= pieces) v[k] = make_float4(kLowest, 0.0f, kLowest, 0.0f), o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+            const float t0 = fmaxf(fmaxf(fmaxf(m[0], v[0].x), fmaxf(v[1].x, v[2].x)), v[3].x);
+            const float t1 = fmaxf(fmaxf(fmaxf(m[1], v[0].z), fmaxf(v[1].z, v[2].z)), v[3].z);
+            const float f0 = exp2_fast(m[0] - t0), f1 = exp2_fast(m[1] - t1);
+            m[0] = t0;
+            m[1] = t1;
+            l[0] *= f0;
+            l[1] *= f1;
+            a[0] *= f0;
+            a[1] *= f1;
+            a[2] *= f0;
+            a[3] *= f1;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float w0 = exp2_fast(v[k].x - t0), w1 = exp2_fast(v[k].z - t1);
+                l[0] += v[k].y * w0;
+                l[1] += v[k].w * w1;
+                a[0] += o[k].x * w0;
+                a[1] += o[k].y * w1;
+                a[2] += o[k].z * w0;
+                a[3] += o[k].w * w1;
             }
         }
-        __syncthreads();
+        if (shift > 0) {
+            sums[warp][lane] = make_float4(a[0], a[1], a[2], a[3]);
+            if (g == 0) ml[warp][c] = make_float4(m[0], l[0], m[1], l[1]);
+            __syncthreads();
+            l[0] = l[1] = a[0] = a[1] = a[2] = a[3] = 0.0f;
+#pragma unroll 1
+            for (int w = first; w < first + (1 << shift) && mine == 0; ++w) {
+                m[0] = fmaxf(m[0], ml[w][c].x);
+                m[1] = fmaxf(m[1], ml[w][c].z);
+            }
+#pragma unroll 1
+            for (int w = first; w < first + (1 << shift) && mine == 0; ++w) {
+                const float4 v = ml[w][c], o = sums[w][lane];
+                const float f0 = exp2_fast(v.x - m[0]), f1 = exp2_fast(v.z - m[1]);
+                l[0] += v.y * f0;
+                l[1] += v.w * f1;
+                a[0] += o.x * f0;
+                a[1] += o.y * f1;
+                a[2] += o.z * f0;
+                a[3] += o.w * f1;
+            }
+            __syncthreads();
+        }
+        if (mine == 0 && item < items) {
+            const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
+            const int h = hk * p.group + sub * 8 + 2 * c, heads = min(8, p.group - sub * 8) - 2 * c;
+            const float gv = __ldg(p.gv);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                if (n < heads) {
+                    const float f = l[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(l[n], gv));
+                    *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(h + n) * p.os_h + (dim / 8) * g + 2 * j) =
+                        bf16x2_from_f32(a[n] * f, a[n + 2] * f);
+                    if (j == 0 && g == 0 && p.lse != nullptr) p.lse[(int64_t)b * p.heads_q + h + n] = lse_of(m[n], l[n]);
+                }
+            }
+        }
     }
 }
 
@@ -1051,10 +1007,10 @@ cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t 
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-template <int kD>
+template <int kD, bool kTma, int kPartsShift>
 cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
     static std::atomic<uint64_t> ready{0};               // devices (below 64) with the shared memory allowed
-    const void *kernel = (const void *)k_paged_attention<kD>;
+    const void *kernel = (const void *)k_paged_attention<kD, kTma, kPartsShift>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -1069,12 +1025,26 @@ cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStr
                             (size_t)p.plan.smem, s, args);
 }
 
+template <int kD>
+cudaError_t launch_parts(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
+    switch ((p.tma ? 4 : 0) + p.plan.parts_shift) {
+        case 0: return launch_main<kD, false, 0>(p, maps, s);
+        case 1: return launch_main<kD, false, 1>(p, maps, s);
+        case 2: return launch_main<kD, false, 2>(p, maps, s);
+        case 3: return launch_main<kD, false, 3>(p, maps, s);
+        case 4: return launch_main<kD, true, 0>(p, maps, s);
+        case 5: return launch_main<kD, true, 1>(p, maps, s);
+        case 6: return launch_main<kD, true, 2>(p, maps, s);
+        default: return launch_main<kD, true, 3>(p, maps, s);
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_paged_attention(const PagedAttnParams &p, const PagedMaps &maps, int dim, cudaStream_t s) {
-    cudaError_t e = dim == 64 ? launch_main<64>(p, maps, s)
-                    : dim == 128 ? launch_main<128>(p, maps, s)
-                                 : launch_main<256>(p, maps, s);
+    cudaError_t e = dim == 64 ? launch_parts<64>(p, maps, s)
+                    : dim == 128 ? launch_parts<128>(p, maps, s)
+                                 : launch_parts<256>(p, maps, s);
     if (e != cudaSuccess) return e;
     // the sequences that can be cut; CTAs for a warp an item, and where the
     // sequences are few, up to a CTA an item, within about four an SM

@@ -284,13 +284,13 @@ __global__ void k_kv_read(KvReadParams p);
 // heads.  The 8 computing warps of a CTA are heads_cta x subs x parts (powers
 // of two): neighbouring KV heads, units of one head, and 16-token parts of
 // the tile of 16 x parts tokens that a stage of the ring holds.
-constexpr int kPagedMaxRanges = 296;
+// Four units a CTA: whole 256-byte pieces of a cache row of 128-value heads;
+// 8 units were 2 to 6 % slower (twice the parts to join), 2 units 6 to 12 %
+// (each row in more pieces).
+constexpr int kPagedUnitsCta = 4;
 constexpr int kPagedMaxStages = 8;
 constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
 constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
-#ifndef PU
-#define PU 4
-#endif
 struct PagedPlan {
     int units_head, units;                   // units of a KV head, of all
     int heads_shift, subs_shift, parts_shift, tile_shift;
@@ -303,7 +303,7 @@ inline PagedPlan paged_plan(int heads_q, int heads_kv, int dim) {
     n.units = heads_kv * n.units_head;
     n.subs_shift = n.units_head % 4 == 0 ? 2 : n.units_head % 2 == 0 ? 1 : 0;
     n.heads_shift = 0;
-    while ((2 << (n.heads_shift + n.subs_shift)) <= PU && heads_kv % (2 << n.heads_shift) == 0) ++n.heads_shift;
+    while ((2 << (n.heads_shift + n.subs_shift)) <= kPagedUnitsCta && heads_kv % (2 << n.heads_shift) == 0) ++n.heads_shift;
     n.parts_shift = 3 - n.subs_shift - n.heads_shift;
     n.tile_shift = 4 + n.parts_shift;
     n.blocks = (heads_kv >> n.heads_shift) * (n.units_head >> n.subs_shift);
@@ -344,14 +344,16 @@ struct PagedAttnParams {
     int32_t sequences, heads_q, group, page_size;
     FastDiv page_div;
     PagedPlan plan;
+    FastDiv sub_blocks;      // CTAs over the units of a head
     int32_t tma;             // page_size % 16 == 0 (16 tokens share a page) and 16-byte scale rows: tiles by TMA
     long long timeout;       // clock bound of a wait
     float scale;
     uint16_t *o;
     int64_t os_b, os_h;
     float *lse;              // nullptr, or [sequences][heads_q]
-    float *part_o;           // [2 ranges][units][8 * dim], in the order of the MMA's lanes
-    float2 *part_ml;         // [2 ranges][units][8]
+    // [2 ranges][units][dim / 16][lane]: values of an M-tile of O^T in a lane
+    float4 *part_o;
+    float4 *part_ml;         // [2 ranges][units][4]: (m, l) of heads 2c and 2c + 1
     int4 *joins;             // (sequence, first range, parts): by sequence, or by range if there are more sequences
     uint32_t *status;
 };
