@@ -628,6 +628,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     bool starts_here = start.tile == 0;
     int left = count, stage = 0;
     uint32_t phase = 0;
+    bool ready = false;
     const uint8_t *ring_at = smem_raw + (ring - smem_u32(smem_raw)), *at = ring_at;
     // the warps' O, where several share a unit's tokens
     float4 *sums = reinterpret_cast<float4 *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
@@ -677,10 +678,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         for (int tile = n_tiles; tile > 0; --tile) {
             // A wait that gives up leaves the CTA in step: its tiles then
             // count as empty, every barrier is still met.
-            if (!failed && !__all_sync(0xFFFFFFFFu, mbar_try_wait(&full[stage], phase))) {
+            if (!failed && !ready) {
                 failed = !__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, p.timeout));
                 if (failed) set_status(p.status, ST_TIMEOUT);
             }
+            const int next = stage + 1 == plan.stages ? 0 : stage + 1;
             const uint32_t mask = failed ? 0u : (uint32_t)masks[stage][part];
 
             // ---- S = K q^T
@@ -719,6 +721,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     mma_f16(s, x[2], y[2], x[3], y[3], qb[2 * step + 2], qb[2 * step + 3]);
                 }
             }
+            // whether the next tile is there: asked now, so that the answer is at hand
+            ready = __all_sync(0xFFFFFFFFu, mbar_test_wait(&full[next], next == 0 ? phase ^ 1u : phase));
             // ---- weights: e = S c - m', rows tk and tk + 8, heads 2c and 2c + 1
             float e[4];
 #pragma unroll
