@@ -910,7 +910,8 @@ nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_hea
         (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 != 0)
         return NVFP4_ERR_ALIGNMENT;
     const int64_t row_blocks = K->cols / 16;
-    if (tokens > INT32_MAX / (2 * row_blocks)) return NVFP4_ERR_SHAPE;      // items are counted in 31 bits
+    // items, and a step past them, are counted in 31 bits
+    if (tokens > (INT32_MAX - (1 << 22)) / (2 * row_blocks)) return NVFP4_ERR_SHAPE;
     int sms = 0;
     st = current_device(&sms);
     if (st != NVFP4_OK) return st;
@@ -946,8 +947,7 @@ nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_hea
     p.per_head_k = fast_div((uint32_t)head_k);
     p.per_head_v = fast_div((uint32_t)head_v);
     p.status = static_cast<uint32_t *>(workspace);
-    // a wave of CTAs at most: each fills its tables once
-    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(p.items, 256), 8LL * sms);
+    const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(p.items, 256), (int64_t)kWriteCtasPerSm * sms);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (d_table == nullptr)
         k_kv_write<<<grid, 256, 0, s>>>(p);

@@ -226,10 +226,7 @@ struct RopeParams {
     uint32_t *status;
 };
 constexpr int kRopeItems = 2;   // interleaved layout: items a thread takes, 256 apart
-#ifndef RH
-#define RH 4
-#endif
-constexpr int kRopeHeads = RH;   // half layout: heads an item takes
+constexpr int kRopeHeads = 4;   // half layout: heads an item takes
 __global__ void k_rope_table(const double *inv_freq, int32_t pairs, int64_t first, int64_t n,
                              double magnitude, float2 *table);
 __global__ void k_rope_half(RopeParams p);
@@ -250,13 +247,14 @@ struct KvWriteParams {
     int64_t table_rows;
     int32_t pairs;
     int32_t interleaved;
-    // items of one or two blocks: tokens x (items of a K row + items of a V row)
-    uint32_t items, k_items; // all; of a K row
-    FastDiv per_token;       // items of a token
+    // items of one or two blocks
+    uint32_t items, k_items; // tokens x (items of a K row + items of a V row); of a K row
+    FastDiv per_token;
     FastDiv per_head_k, per_head_v;
     uint32_t head_blocks;
     uint32_t *status;
 };
+constexpr int kWriteCtasPerSm = 3;   // one wave of CTAs, each thread an item ahead
 __global__ void k_kv_write(KvWriteParams p);
 __global__ void k_kv_write_half(KvWriteParams p);
 __global__ void k_kv_write_any(KvWriteParams p);

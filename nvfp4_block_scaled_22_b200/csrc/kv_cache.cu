@@ -8,13 +8,19 @@
 // scales; per 16-value block the steps of nvfp4_quantize with a supplied g,
 //   s = e4m3(RN(RN(amax / 6) g)),  e = s ? RN(g / s) : 0,
 //   code = e2m1(RN(x e)),
-// so the bytes are those of nvfp4_quantize of the (rotated) rows; the two
-// divisions come from tables that a CTA fills once (they would be a third of
-// the instructions otherwise).  A thread takes two blocks at a time: a pair
-// that the half layout rotates into each other, or two neighbours.
+// so the bytes are those of nvfp4_quantize of the (rotated) rows.  A thread
+// takes two blocks at a time: a pair that the half layout rotates into each
+// other, or two neighbours.
 // k_kv_read: y = bf16(RN(e2m1 RN(s / g))), the steps of nvfp4_dequantize.
 //
-// Both are bound by memory (2.56 bytes a value).
+// Both are bound by memory (2.56 bytes a value): 131072 rows of 2 x 1024
+// values are read back in 108 us (6.4 TB/s), 16384 tokens of 2 x 8 x 128
+// written in 17.9 us (4.8 TB/s, launch included), with rotated keys in 24.7
+// us -- a key block then costs 12 instructions a value, on loads that wait
+// for the position and then for the table row.  Tried for the write: a half
+// block a thread (30 us: the scale's arithmetic twice), two heads a thread
+// that share table entries (27.6 us: registers), tables for the divisions
+// (26.5 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -105,71 +111,100 @@ __device__ __forceinline__ void rotate_alone(Block &a, const uint16_t *x, int bl
     a.hi = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
+// One block under the tensor scale g (div6_f32 is RN(amax / 6)).
+__device__ __forceinline__ EncodeBlockOut encode(const Block &x, float g) {
+    const uint32_t bits = block_amax_bits(x.lo, x.hi);
+    EncodeBlockOut o;
+    o.scale = e4m3_from_f32(__fmul_rn(div6_f32(__uint_as_float(bits)), g));
+    const uint32_t s = o.scale & 0x7Fu;
+    const float e = s == 0u || s == 0x7Fu ? 0.0f : __fdiv_rn(g, f32_from_e4m3(s));
+    o.codes.x = encode8(x.lo.x, x.lo.y, x.lo.z, x.lo.w, e);
+    o.codes.y = encode8(x.hi.x, x.hi.y, x.hi.z, x.hi.w, e);
+    o.finite = bits <= 0x7F7FFFFFu;
+    return o;
+}
+
+// One or two blocks of a head, with what their writing needs.
+struct WriteItem {
+    Block a, b;
+    const uint16_t *x;
+    int32_t slot, position;
+    int b0, b1, h;           // blocks (b1: -1 if there is one), head
+    bool is_v, turns;        // the blocks are rotated into each other
+};
+
 // kRope: 0 no rotation, 1 half layout with whole partner blocks (pairs % 16
 // == 0), 2 any other.
 template <int kRope>
-__device__ __forceinline__ void kv_write_body(const KvWriteParams &p) {
-    __shared__ EncodeTables tables[2];
-    const float gk = *p.gk, gv = *p.gv;
-    fill_tables(tables[0], gk);
-    fill_tables(tables[1], gv);
-    __syncthreads();
+__device__ __forceinline__ WriteItem fetch_item(const KvWriteParams &p, uint32_t item) {
+    WriteItem w;
+    const uint32_t t = quotient(item, p.per_token);
+    uint32_t rest = item - t * p.per_token.d;                       // of the K row, then of the V row
+    w.is_v = rest >= p.k_items;
+    if (w.is_v) rest -= p.k_items;
+    w.h = (int)quotient(rest, w.is_v ? p.per_head_v : p.per_head_k);
+    const int i = (int)rest - w.h * (int)(w.is_v ? p.per_head_v.d : p.per_head_k.d);
+    w.slot = p.slots[t];
+    w.position = kRope != 0 ? p.positions[t] : 0;
+    w.x = w.is_v ? p.v + (int64_t)t * p.vs_t + w.h * p.vs_h : p.k + (int64_t)t * p.ks_t + w.h * p.ks_h;
     // items of a head: pairs of rotated blocks (kRope 1), then two neighbours at a time
-    const int turned = kRope == 1 ? p.pairs >> 4 : 0;
-    const int head_blocks = (int)p.head_blocks;
-#pragma unroll 1
-    for (uint32_t item = blockIdx.x * 256u + threadIdx.x; item < p.items; item += gridDim.x * 256u) {
-        const uint32_t t = quotient(item, p.per_token);
-        uint32_t rest = item - t * p.per_token.d;                   // of the K row, then of the V row
-        const bool is_v = rest >= p.k_items;
-        if (is_v) rest -= p.k_items;
-        const uint32_t h = quotient(rest, is_v ? p.per_head_v : p.per_head_k);
-        const int i = (int)(rest - h * (is_v ? p.per_head_v.d : p.per_head_k.d));
-        // the values are fetched before the slot is known to be one
-        const int32_t slot = p.slots[t], position = kRope != 0 ? p.positions[t] : 0;
-        const uint16_t *x = is_v ? p.v + (int64_t)t * p.vs_t + (int64_t)h * p.vs_h
-                                 : p.k + (int64_t)t * p.ks_t + (int64_t)h * p.ks_h;
-        int b0, b1;
-        if (kRope == 1 && !is_v && i < turned) {
-            b0 = i;
-            b1 = i + turned;
-        } else {
-            b0 = is_v ? 2 * i : 2 * turned + 2 * (i - turned);
-            b1 = b0 + 1 < head_blocks ? b0 + 1 : -1;
-        }
-        Block a = load_block(x + 16 * b0), b = a;
-        if (b1 >= 0) b = load_block(x + 16 * b1);
-        const int64_t row = pool_row(slot, p.pool_rows, p.status);
+    const int turned = kRope == 1 && !w.is_v ? p.pairs >> 4 : 0;
+    w.turns = i < turned;
+    w.b0 = w.turns ? i : 2 * turned + 2 * (i - turned);
+    w.b1 = w.turns ? i + turned : w.b0 + 1 < (int)p.head_blocks ? w.b0 + 1 : -1;
+    w.a = load_block(w.x + 16 * w.b0);
+    w.b = load_block(w.x + 16 * (w.b1 >= 0 ? w.b1 : w.b0));
+    return w;
+}
+
+template <int kRope>
+__device__ __forceinline__ void write_item(const KvWriteParams &p, WriteItem &w) {
+    const int64_t row = pool_row(w.slot, p.pool_rows, p.status);
+    if (row < 0) return;
+    if (kRope != 0) {
         // a token whose position has no table row is not written at all
-        const int64_t pos = row >= 0 && kRope != 0 ? rope_row(position, p.table_rows, p.status) : 0;
-        if (row < 0 || pos < 0) continue;
-        if (!is_v) {
-            if (kRope == 1 && i < turned) rotate_blocks(a, b, p.table + pos * p.pairs + 16 * i);
-            if (kRope == 2) {
-                rotate_alone(a, x, b0, p, pos);
-                if (b1 >= 0) rotate_alone(b, x, b1, p, pos);
-            }
-        }
-        const float g = is_v ? gv : gk;
-        const EncodeTables &tab = tables[is_v ? 1 : 0];
-        const EncodeBlockOut ea = encode_block(a.lo, a.hi, g, tab), eb = encode_block(b.lo, b.hi, g, tab);
-        if (!ea.finite || !eb.finite) set_status(p.status, ST_NONFINITE);
-        uint8_t *c = (is_v ? p.vc : p.kc) + row * p.row_codes + (int64_t)h * head_blocks * 8;
-        uint8_t *sc = (is_v ? p.vs : p.ks) + row * p.row_scales + (int64_t)h * head_blocks;
-        *reinterpret_cast<uint2 *>(c + 8 * b0) = ea.codes;
-        sc[b0] = (uint8_t)ea.scale;
-        if (b1 >= 0) {
-            *reinterpret_cast<uint2 *>(c + 8 * b1) = eb.codes;
-            sc[b1] = (uint8_t)eb.scale;
+        const int64_t pos = rope_row(w.position, p.table_rows, p.status);
+        if (pos < 0) return;
+        if (kRope == 1 && w.turns) rotate_blocks(w.a, w.b, p.table + pos * p.pairs + 16 * w.b0);
+        if (kRope == 2 && !w.is_v) {
+            rotate_alone(w.a, w.x, w.b0, p, pos);
+            if (w.b1 >= 0) rotate_alone(w.b, w.x, w.b1, p, pos);
         }
     }
+    const float g = __ldg(w.is_v ? p.gv : p.gk);
+    uint8_t *codes = (w.is_v ? p.vc : p.kc) + row * p.row_codes + (int64_t)w.h * p.head_blocks * 8;
+    uint8_t *scales = (w.is_v ? p.vs : p.ks) + row * p.row_scales + (int64_t)w.h * p.head_blocks;
+    const EncodeBlockOut ea = encode(w.a, g), eb = encode(w.b, g);
+    if (!ea.finite || !eb.finite) set_status(p.status, ST_NONFINITE);
+    *reinterpret_cast<uint2 *>(codes + 8 * w.b0) = ea.codes;
+    scales[w.b0] = (uint8_t)ea.scale;
+    if (w.b1 >= 0) {
+        *reinterpret_cast<uint2 *>(codes + 8 * w.b1) = eb.codes;
+        scales[w.b1] = (uint8_t)eb.scale;
+    }
+}
+
+// Each thread fetches its next item before it works on the one it has.
+template <int kRope>
+__device__ __forceinline__ void kv_write_body(const KvWriteParams &p) {
+    const uint32_t step = gridDim.x * 256u;
+    uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    if (item >= p.items) return;
+    WriteItem now = fetch_item<kRope>(p, item);
+#pragma unroll 1
+    for (; item + step < p.items; item += step) {
+        const WriteItem next = fetch_item<kRope>(p, item + step);
+        write_item<kRope>(p, now);
+        now = next;
+    }
+    write_item<kRope>(p, now);
 }
 
 }  // namespace
 
-__global__ void __launch_bounds__(256) k_kv_write(KvWriteParams p) { kv_write_body<0>(p); }
-__global__ void __launch_bounds__(256) k_kv_write_half(KvWriteParams p) { kv_write_body<1>(p); }
-__global__ void __launch_bounds__(256) k_kv_write_any(KvWriteParams p) { kv_write_body<2>(p); }
+__global__ void __launch_bounds__(256, kWriteCtasPerSm) k_kv_write(KvWriteParams p) { kv_write_body<0>(p); }
+__global__ void __launch_bounds__(256, kWriteCtasPerSm) k_kv_write_half(KvWriteParams p) { kv_write_body<1>(p); }
+__global__ void __launch_bounds__(256, kWriteCtasPerSm) k_kv_write_any(KvWriteParams p) { kv_write_body<2>(p); }
 
 // Four blocks a thread, 256 apart, loaded before the first is stored.
 __global__ void __launch_bounds__(256) k_kv_read(KvReadParams p) {

@@ -11,7 +11,8 @@
 // FP64: a position times a frequency needs about 24 + 20 bits before it is
 // reduced to a turn, so an FP32 angle is off by 0.06 at position 2^20.
 //
-// Bound by memory: 4 bytes a value against 3 FP32 operations.
+// Bound by memory: 4 bytes a value against 3 FP32 operations (8192 x 72 x 128
+// in 47.8 us, 6.4 TB/s; 4099 x 40 x 128 interleaved, half rotated, in 13.9 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ RopeItem rope_item(const RopeParams &p, uint32_t item
 // Half layout: an item is 8 pairs (two 16-byte pieces) of kRopeHeads heads
 // of a token, which share 64 bytes of the table; then the 8-value pieces
 // behind the rotated part.  With an item a head, the table took twice the
-// L1 traffic of the values (58 us against 50 at 8192 x 72 x 128).  All heads
+// L1 traffic of the values (55.6 us against 47.8 at 8192 x 72 x 128).  All heads
 // are loaded before one is stored (y may be x, so that the compiler would
 // not).
 __global__ void __launch_bounds__(256) k_rope_half(RopeParams p) {
