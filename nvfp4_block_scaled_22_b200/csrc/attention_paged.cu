@@ -63,6 +63,7 @@ constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' mo
 constexpr int kWarps = 8;            // warps that compute
 constexpr int kProducers = 2;       // warps that bring the tiles in, stages in turn
 constexpr int kThreads = 32 * (kWarps + kProducers);
+constexpr long long kDrainCycles = 2000000000ll;   // bound of the wait for copies under way (about a second)
 constexpr int kTile = 16;            // tokens of a warp's tile
 
 template <int kD>
@@ -102,6 +103,16 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *desc, uint
         " [%0], [%1, {%3, %4, %5}], [%2];"
         :: "r"(dst), "l"(reinterpret_cast<uint64_t>(desc)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+// Wait for a phase of `bar`, at most about `limit` cycles.  (A try may sleep
+// for some microseconds, so that the limit is looked at before each.)
+__device__ __forceinline__ bool bounded_wait(uint64_t *bar, uint32_t parity, long long limit) {
+    const long long t0 = clock64();
+    if (mbar_test_wait(bar, parity)) return true;
+    while (clock64() - t0 <= limit)
+        if (mbar_try_wait(bar, parity)) return true;
+    return false;
 }
 
 // Arrives on `bar` once this thread's cp.async copies so far have landed.
@@ -399,8 +410,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         int left = count, stage = 0;
         uint32_t phase = 1;                                             // of `empty`: the first round passes
         auto acquire = [&]() {
-            if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(&empty[stage], phase))) {
-                failed = !__all_sync(0xFFFFFFFFu, mbar_wait(&empty[stage], phase, p.timeout));
+            if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(&empty[stage], phase))) {
+                failed = !__all_sync(0xFFFFFFFFu, bounded_wait(&empty[stage], phase, p.timeout));
                 if (failed && lane == 0) set_status(p.status, ST_TIMEOUT);
             }
         };
@@ -442,6 +453,10 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 return f;
             };
             const uint32_t bytes = 2u * (part_codes + part_scales);
+            // Stages that this warp has armed, the parity of their `full`, and
+            // those that no later tile uses.
+            uint32_t armed = 0, parity = 0, last = 0;
+            int tiles_left = count;                                     // from the first of the batch
             Batch f = lookup();
             while (f.n > 0) {
                 const Batch next = lookup();
@@ -456,6 +471,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         advance();
                         continue;
                     }
+                    const int tile = count - tiles_left + i;
                     const int from = (i << kPartsShift) + my_part;
                     const int my_row = __shfl_sync(0xFFFFFFFFu, row, from);
                     const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, from);
@@ -465,6 +481,9 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     if (lane < tw) masks[stage][lane] = (1 << tokens) - 1;
                     __syncwarp();
                     if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(there) * bytes);
+                    armed |= 1u << stage;
+                    parity = (parity & ~(1u << stage)) | ((phase ^ 1u) << stage);
+                    if (tile + plan.stages >= count) last |= 1u << stage;
                     uint32_t to = ring + stage * plan.stage_bytes, scales = to + k_scales;
 #pragma unroll 1
                     for (int n = 0; n < tw; ++n, to += part_codes, scales += part_scales) {
@@ -480,8 +499,15 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     advance();
                 }
                 if (failed) break;
+                tiles_left -= f.n;
                 f = next;
             }
+            // No copy may be under way when the CTA ends, whoever has given up
+            // waiting for it.
+            const uint32_t await = failed ? armed : last;
+#pragma unroll 1
+            for (int n = 0; n < plan.stages; ++n)
+                if ((await >> n) & 1u) bounded_wait(&full[n], (parity >> n) & 1u, kDrainCycles);
         } else {
             // Pages that end inside of a tile, or rows that TMA cannot step
             // by: the rows of a stage's tokens are looked up one stage ahead,
@@ -568,13 +594,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 advance();
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-        }
-        if (failed) {
-            // copies may be under way into stages that nobody waits for
-            for (int n = 0; n < plan.stages; ++n) {
-                mbar_wait(&full[n], 0u, p.timeout);
-                mbar_wait(&full[n], 1u, p.timeout);
-            }
         }
         return;
     }
@@ -679,7 +698,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             // A wait that gives up leaves the CTA in step: its tiles then
             // count as empty, every barrier is still met.
             if (!failed && !ready) {
-                failed = !__all_sync(0xFFFFFFFFu, mbar_wait(&full[stage], phase, p.timeout));
+                failed = !__all_sync(0xFFFFFFFFu, bounded_wait(&full[stage], phase, p.timeout));
                 if (failed) set_status(p.status, ST_TIMEOUT);
             }
             const int next = stage + 1 == plan.stages ? 0 : stage + 1;
@@ -817,8 +836,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 
         // ---- end of this CTA's part of the sequence: the unit's warps meet
         // in shared memory, and each sums and stores its share of the M-tiles.
-        // Compact on purpose: this code is cold when it is reached, and cold
-        // straight-line code costs some 40 cycles an instruction to fetch.
+        // Rolled loops on purpose: with everything unrolled the kernel was
+        // 131 KB, and fetching it made a one-token call 10.8 us, not 8.9.
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -828,8 +847,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         for (int j = 0; j < S::kSteps; ++j) mine[32 * j] = make_float4(oacc[j][0], oacc[j][1], oacc[j][2], oacc[j][3]);
         if (g == 0) ml[warp][c] = make_float4(mp[0], lsum[0], mp[1], lsum[1]);
         const int step = kWarps >> kPartsShift;                    // warps between two parts of a unit
-        if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
-        else warp_sync();
+        unit_barrier(1 + unit_cta, 32 * tw);
         float M[2] = {kLowest, kLowest}, L[2] = {0.0f, 0.0f};
 #pragma unroll 1
         for (int w = unit_cta; w < kWarps; w += step) {
@@ -884,8 +902,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             }
         }
         // what is read above is written again only behind the next barrier of the unit
-        if (tw > 1) unit_barrier(1 + unit_cta, 32 * tw);
-        else warp_sync();
+        unit_barrier(1 + unit_cta, 32 * tw);
         if (left == 0) break;
         ++b;
         in_seq = tiles_of(length_of(p, b), (4 + kPartsShift));
@@ -1029,18 +1046,23 @@ cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStr
                             (size_t)p.plan.smem, s, args);
 }
 
+// Parts that the plan can ask for: with TMA a row's scales are whole 16-byte
+// groups, so that there are at least 4 heads of 64 or 2 of 128 values.
 template <int kD>
 cudaError_t launch_parts(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
-    switch ((p.tma ? 4 : 0) + p.plan.parts_shift) {
-        case 0: return launch_main<kD, false, 0>(p, maps, s);
-        case 1: return launch_main<kD, false, 1>(p, maps, s);
-        case 2: return launch_main<kD, false, 2>(p, maps, s);
-        case 3: return launch_main<kD, false, 3>(p, maps, s);
-        case 4: return launch_main<kD, true, 0>(p, maps, s);
-        case 5: return launch_main<kD, true, 1>(p, maps, s);
-        case 6: return launch_main<kD, true, 2>(p, maps, s);
-        default: return launch_main<kD, true, 3>(p, maps, s);
+    const int parts = p.plan.parts_shift;
+    if (p.tma) {
+        if (parts == 1) return launch_main<kD, true, 1>(p, maps, s);
+        if constexpr (kD >= 128)
+            if (parts == 2) return launch_main<kD, true, 2>(p, maps, s);
+        if constexpr (kD == 256)
+            if (parts == 3) return launch_main<kD, true, 3>(p, maps, s);
+    } else {
+        if (parts == 1) return launch_main<kD, false, 1>(p, maps, s);
+        if (parts == 2) return launch_main<kD, false, 2>(p, maps, s);
+        if (parts == 3) return launch_main<kD, false, 3>(p, maps, s);
     }
+    return cudaErrorInvalidConfiguration;
 }
 
 }  // namespace

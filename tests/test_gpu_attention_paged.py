@@ -91,6 +91,33 @@ def test_ragged_batches(lens, heads, group, dim, page):
     _check(cache, q, o, lse, dim ** -0.5)
 
 
+# The kernel has a form per head size, per way of copying (TMA where 16 tokens
+# share a page and a row's scales are whole 16-byte groups) and per warps of a
+# unit (2, 4, 8); the cases above and below meet each of them.
+@pytest.mark.parametrize("lens,heads,group,dim,page", [
+    ([700, 33, 16], 4, 8, 64, 16), ([129, 0, 90], 8, 12, 64, 32), ([300, 41], 1, 40, 64, 16), ([260], 4, 30, 128, 20),
+    ([350, 70], 2, 32, 128, 16), ([90, 200, 5], 2, 16, 128, 48), ([400, 8], 6, 2, 128, 16), ([77, 500], 4, 4, 256, 16),
+    ([300, 30], 1, 5, 256, 32), ([200, 64], 4, 8, 256, 20), ([150, 6], 2, 1, 256, 9), ([330, 11], 1, 8, 256, 7),
+    ([130, 1], 1, 9, 256, 24), ([610, 2, 48], 3, 16, 256, 16)])
+def test_every_form_of_the_kernel(lens, heads, group, dim, page):
+    cache = Cache(lens, heads, dim, page, sum(lens) + group)
+    q = _query(len(lens), heads * group, dim, 31)
+    o, lse = cache.attend(q.to(DEV))
+    _check(cache, q, o, lse, dim ** -0.5)
+
+
+def test_batch_of_sequences_that_are_all_cut():
+    """60 sequences (more than a warp schedules by itself) over 148 ranges:
+    each is cut and joined, some from two parts, some from more."""
+    rng = np.random.default_rng(33)
+    lens = [int(v) for v in rng.integers(150, 900, 60)]
+    lens[7], lens[8] = 0, 3000
+    cache = Cache(lens, 4, 64, 16, 34)
+    q = _query(60, 16, 64, 35)
+    o, lse = cache.attend(q.to(DEV))
+    _check(cache, q, o, lse, 0.125)
+
+
 @pytest.mark.parametrize("n,heads,dim", [(20000, 2, 128), (9001, 1, 64), (5000, 2, 256)])
 def test_one_long_sequence_split_over_the_device(n, heads, dim):
     """Also peaked weights in the last tokens, after which all that was summed
@@ -304,6 +331,25 @@ def test_captured_step_replayed_with_other_lengths_and_pages():
         _check(view, turned[0], o, lse, dim ** -0.5, f"replay {i}")
         lens += 1
     assert nb.nvfp4_check_status() == 0
+
+
+@pytest.mark.parametrize("heads,dim,page", [(4, 128, 16), (1, 64, 16)])      # TMA, and copies without it
+def test_a_wait_that_gives_up_is_recorded(heads, dim, page):
+    """The wait limit cut to one cycle: the first wait that does not find its
+    tile there gives up, the call records it and ends by itself; the next
+    call is right."""
+    cache = Cache([3000, 500], heads, dim, page, 40)
+    q = _query(2, heads * 4, dim, 41)
+    ws = nb.Workspace(DEV, 256)
+    nb.nvfp4_set_wait_limit_cycles(1)
+    try:
+        cache.attend(q.to(DEV), workspace=ws)
+        assert nb.nvfp4_check_status(ws) == 7
+    finally:
+        nb.nvfp4_set_wait_limit_cycles(0)
+    o, lse = cache.attend(q.to(DEV), workspace=ws)
+    assert nb.nvfp4_check_status(ws) == 0
+    _check(cache, q, o, lse, dim ** -0.5)
 
 
 def test_binding_refusals():
