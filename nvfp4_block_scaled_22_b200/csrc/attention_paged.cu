@@ -640,7 +640,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         vs_at = v_scales + scales + (kD == 64 ? g >> 1 : kD == 128 ? g : 2 * g);
     }
 
-    uint32_t qb[2 * S::kSteps];          // B fragments of the query
+    // the warps' O, where several share a unit's tokens
+    float4 *sums = reinterpret_cast<float4 *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
+    // B fragments of the query, kept where the warp's sums go later: registers
+    // are what limits the warps of an SM here
+    uint4 *q_frag = reinterpret_cast<uint4 *>(sums + warp * (2 * kD)) + lane;
     float oacc[S::kSteps][4];
     float lsum[2], mp[2], ck[2];
     int b = start.b, in_seq = start.tiles - start.tile;        // tiles to the end of the sequence
@@ -649,8 +653,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     uint32_t phase = 0;
     bool ready = false;
     const uint8_t *ring_at = smem_raw + (ring - smem_u32(smem_raw)), *at = ring_at;
-    // the warps' O, where several share a unit's tokens
-    float4 *sums = reinterpret_cast<float4 *>(smem_raw + (ring - smem_u32(smem_raw)) + plan.stages * plan.stage_bytes);
 
     while (true) {
         {   // query of head g: lane c holds dims kD / 4 * c ... (kD = 256: 32c .. + 31 and 128 + 32c .. + 31)
@@ -675,9 +677,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
             for (int n = 0; n < kD / 32; ++n) {
                 const uint32_t x[4] = {w[n].x, w[n].y, w[n].z, w[n].w};
+                uint32_t y[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    qb[4 * n + k] = f16x2_from_f32(__fmul_rn(bf16_lo(x[k]), mult), __fmul_rn(bf16_hi(x[k]), mult));
+                    y[k] = f16x2_from_f32(__fmul_rn(bf16_lo(x[k]), mult), __fmul_rn(bf16_hi(x[k]), mult));
+                q_frag[32 * n] = make_uint4(y[0], y[1], y[2], y[3]);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -735,9 +739,25 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         x[k] = mul_f16x2(x[k], s0[blk]);
                         y[k] = mul_f16x2(y[k], s1[blk]);
                     }
-                    const int step = 8 * part_k + 2 * n;
-                    mma_f16(s, x[0], y[0], x[1], y[1], qb[2 * step], qb[2 * step + 1]);
-                    mma_f16(s, x[2], y[2], x[3], y[3], qb[2 * step + 2], qb[2 * step + 3]);
+                    const uint4 f = q_frag[32 * (4 * part_k + n)];
+                    mma_f16(s, x[0], y[0], x[1], y[1], f.x, f.y);
+                    mma_f16(s, x[2], y[2], x[3], y[3], f.z, f.w);
+                }
+            }
+            uint32_t wa[2][kVWords], wb[2][kVWords], sc[2][2];          // [rows 2c.. / 2c + 8 ..]
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                lds_words<kVWords>(at + va_at + 8 * n * S::kCodes, wa[n]);
+                lds_words<kVWords>(at + vb_at + 8 * n * S::kCodes, wb[n]);
+                if (kD == 256) {
+                    const uint32_t x = lds16(at + vs_at + (ta + 8 * n) * 16);
+                    const uint32_t y = lds16(at + vs_at + (tb + 8 * n) * 16);
+                    sc[n][0] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0040));
+                    sc[n][1] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0051));
+                } else {
+                    const uint32_t x = lds8(at + vs_at + (ta + 8 * n) * 16);
+                    const uint32_t y = lds8(at + vs_at + (tb + 8 * n) * 16);
+                    sc[n][0] = sc[n][1] = f16x2_from_e4m3x2(x | (y << 8));
                 }
             }
             // whether the next tile is there: asked now, so that the answer is at hand
@@ -780,22 +800,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             const uint32_t p1 = transpose_8x8(f16x2_from_f32(e[2], e[3]));
 
             // ---- O^T += V^T P^T
-            uint32_t wa[2][kVWords], wb[2][kVWords], sc[2][2];          // [rows 2c.. / 2c + 8 ..]
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                lds_words<kVWords>(at + va_at + 8 * n * S::kCodes, wa[n]);
-                lds_words<kVWords>(at + vb_at + 8 * n * S::kCodes, wb[n]);
-                if (kD == 256) {
-                    const uint32_t x = lds16(at + vs_at + (ta + 8 * n) * 16);
-                    const uint32_t y = lds16(at + vs_at + (tb + 8 * n) * 16);
-                    sc[n][0] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0040));
-                    sc[n][1] = f16x2_from_e4m3x2(__byte_perm(x, y, 0x0051));
-                } else {
-                    const uint32_t x = lds8(at + vs_at + (ta + 8 * n) * 16);
-                    const uint32_t y = lds8(at + vs_at + (tb + 8 * n) * 16);
-                    sc[n][0] = sc[n][1] = f16x2_from_e4m3x2(x | (y << 8));
-                }
-            }
             if (mask != 0xFFFFu) {
                 // what lies in the rows of absent tokens is not theirs: with
                 // a scale of 0 their values count 0 (any code is finite)
