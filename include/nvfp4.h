@@ -396,7 +396,8 @@ NVFP4_API nvfp4_status nvfp4_rope_table(const double *d_inv_freq, int32_t rotary
  *   2-byte aligned; 16-byte aligned pieces (strides % 8 == 0, rotary_dim % 16
  *   == 0, or % 8 if interleaved) take the vectorised path.
  * d_positions: int32[tokens]; position -1 leaves the token's y as it was.
- * rotary_dim: even, 2 .. head_dim.  tokens * heads * head_dim < 2^31 pieces. */
+ * rotary_dim: even, 2 .. head_dim.  tokens * heads * head_dim < 2^31 always
+ *   fits (more does on the vectorised path; else NVFP4_ERR_SHAPE). */
 NVFP4_API nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride,
                                   int64_t tokens, int32_t heads, int32_t head_dim,
                                   const int32_t *d_positions, const float *d_table,
@@ -413,8 +414,8 @@ NVFP4_API nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t
  * d_table == NULL: no rotation, the rotary arguments are ignored.
  * k, v: BF16 [tokens][heads][head_dim], strides in elements, multiples of 8;
  *   16-byte aligned.  head_dim % 16 == 0, heads * head_dim == K->cols.
- * Two tokens of one call may not name the same slot (the row would hold parts
- * of both).  Non-finite values are recorded as NVFP4_ERR_NONFINITE; the
+ * Two tokens of one call may not name the same slot, nor K and V share their
+ * buffers unless equal bytes go there (the row would hold parts of both).  Non-finite values are recorded as NVFP4_ERR_NONFINITE; the
  * 16-value block that holds them is then unspecified. */
 NVFP4_API nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_head_stride,
                                       const void *v, int64_t v_token_stride, int64_t v_head_stride,
@@ -428,7 +429,7 @@ NVFP4_API nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int
 /* Read rows back: k[r], v[r] = BF16 of pool row d_slots[r] of K and V, as
  * nvfp4_dequantize restores them; slot -1 (or out of range) gives zeros.
  * k, v: BF16 [rows x cols], pitches ldk, ldv elements (multiples of 8),
- * 16-byte aligned.  For the dense attention of a prompt chunk over what is
+ * 16-byte aligned, two arrays.  For the dense attention of a prompt chunk over what is
  * cached already. */
 NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V,
                                      const int32_t *d_slots, int64_t rows, void *k, int64_t ldk,
@@ -447,7 +448,9 @@ NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *
  * to it (to 0) and recorded as NVFP4_ERR_INVALID_ARG; tokens on a page
  * outside of the pool take no part and are recorded alike.
  * q, o  : BF16 [sequences][heads_q][head_dim], strides in elements, multiples
- *         of 8; 16-byte aligned.  head_dim = K->cols / heads_kv: 64, 128, 256.
+ *         of 8; 16-byte aligned.  o == q with equal strides works in place;
+ *         they may not overlap in part.  head_dim = K->cols / heads_kv: 64,
+ *         128, 256.  heads_q < 2^16.
  * page_size: any; K->rows a multiple of it and below 2^31.  table_pages *
  *   page_size < 2^31 - 1024, sequences * (table_pages * page_size / 16 + 1) < 2^31.
  * scratch: nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, head_dim)

@@ -967,7 +967,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V, const i
     st = check_workspace(workspace, workspace_bytes, kStatusBytes);
     if (st != NVFP4_OK) return st;
     if (rows == 0 || K->cols == 0) return NVFP4_OK;
-    if (k == nullptr || v == nullptr || d_slots == nullptr) return NVFP4_ERR_INVALID_ARG;
+    if (k == nullptr || v == nullptr || k == v || d_slots == nullptr) return NVFP4_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(d_slots) & 3u) != 0 ||
         ldk % 8 != 0 || ldv % 8 != 0)
         return NVFP4_ERR_ALIGNMENT;
@@ -1003,7 +1003,7 @@ nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V, const i
 }
 
 size_t nvfp4_attention_paged_scratch_bytes(int32_t heads_q, int32_t heads_kv, int32_t head_dim) {
-    if (heads_q < 1 || heads_kv < 1 || heads_q % heads_kv != 0 ||
+    if (heads_q < 1 || heads_q > kPagedMaxHeads || heads_kv < 1 || heads_q % heads_kv != 0 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return 0;
     return paged_scratch_bytes(paged_plan(heads_q, heads_kv, head_dim), head_dim);
@@ -1024,7 +1024,7 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
         page_size < 1 || q_seq_stride < 0 || q_head_stride < 0 || o_seq_stride < 0 ||
         o_head_stride < 0 || !std::isfinite(scale))
         return NVFP4_ERR_INVALID_ARG;
-    if (heads_q % heads_kv != 0 || K->cols % heads_kv != 0) return NVFP4_ERR_SHAPE;
+    if (heads_q > kPagedMaxHeads || heads_q % heads_kv != 0 || K->cols % heads_kv != 0) return NVFP4_ERR_SHAPE;
     const int64_t dim = K->cols / heads_kv;
     if (dim != 64 && dim != 128 && dim != 256) return NVFP4_ERR_SHAPE;
     if (K->rows % page_size != 0 || K->rows > INT32_MAX || K->cols > INT32_MAX) return NVFP4_ERR_SHAPE;
@@ -1047,6 +1047,9 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
           reinterpret_cast<uintptr_t>(d_lse)) & 3u) != 0)
         return NVFP4_ERR_ALIGNMENT;
     if (!rows_apart(o_seq_stride, sequences, o_head_stride, heads_q, dim)) return NVFP4_ERR_SHAPE;
+    // in place each query is read by the warps that write its result, or before the join starts
+    if (q == o && ((sequences > 1 && q_seq_stride != o_seq_stride) || (heads_q > 1 && q_head_stride != o_head_stride)))
+        return NVFP4_ERR_INVALID_ARG;
     int sms = 0;
     st = current_device(&sms);
     if (st != NVFP4_OK) return st;

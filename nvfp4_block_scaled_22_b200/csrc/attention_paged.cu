@@ -247,7 +247,7 @@ __device__ __forceinline__ Ranges ranges_of(uint32_t total, uint32_t ctas) {
     return r;
 }
 
-constexpr int kWarpSchedule = 32;   // up to this many sequences each warp works the schedule out for itself
+constexpr int kWarpSchedule = 32;   // up to this many sequences each warp works the schedule out for itself, one a lane
 
 // What the joining kernel has to know of a sequence that starts in this range.
 __device__ __forceinline__ void write_join(const PagedAttnParams &p, const Ranges &r, int b, uint32_t at, int tiles) {
@@ -301,46 +301,30 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     Cursor start;
     int count;
     if (p.sequences <= kWarpSchedule) {
-        // every warp for itself: a lane holds neighbouring sequences
-        const int per = (p.sequences + 31) >> 5, b0 = lane * per;
-        int lens[kWarpSchedule / 32];
-        uint32_t mine = 0;
-        bool wrong = false;
-#pragma unroll
-        for (int n = 0; n < kWarpSchedule / 32; ++n) {
-            lens[n] = 0;
-            if (n < per && b0 + n < p.sequences) {
-                const int len = __ldg(p.seq_lens + b0 + n);
-                wrong |= len < 0 || len > p.capacity;
-                lens[n] = min(max(len, 0), p.capacity);
-                mine += tiles_of(lens[n], (4 + kPartsShift));
-            }
+        int len = 0;
+        uint32_t tiles = 0;
+        if (lane < p.sequences) {
+            const int given = __ldg(p.seq_lens + lane);
+            len = min(max(given, 0), p.capacity);
+            tiles = tiles_of(len, 4 + kPartsShift);
+            if (given != len && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
         }
-        if (wrong && warp == 0 && blockIdx.x == 0 && blockIdx.y == 0) set_status(p.status, ST_INVALID_ARG);
-        uint32_t upto = mine;
+        uint32_t upto = tiles;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, upto, off);
             if (lane >= off) upto += v;
         }
         const Ranges ranges = ranges_of(__shfl_sync(0xFFFFFFFFu, upto, 31), gridDim.x);
-        const uint32_t first = ranges.first(blockIdx.x), last = ranges.first(blockIdx.x + 1);
+        const uint32_t first = ranges.first(blockIdx.x), last = ranges.first(blockIdx.x + 1), at = upto - tiles;
         count = (int)(last - first);
-        uint32_t at = upto - mine;
-        const bool holds = mine > 0 && at <= first && first < upto;     // one lane, if there are tiles at all
-        const bool joins = warp == 0 && blockIdx.y == 0;
-        start = Cursor{0, 0, 1, 0};
-        if (joins && p.sequences > (int)gridDim.x && lane == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
-        __syncwarp();
-#pragma unroll
-        for (int n = 0; n < kWarpSchedule / 32; ++n) {
-            if (n < per && b0 + n < p.sequences) {
-                const int tiles = tiles_of(lens[n], (4 + kPartsShift));
-                if (at <= first && first < at + tiles) start = Cursor{b0 + n, (int)(first - at), tiles, lens[n]};
-                if (joins && at >= first && at < last) write_join(p, ranges, b0 + n, at, tiles);
-                at += tiles;
-            }
+        const bool holds = at <= first && first < upto;                 // one lane, if there are tiles at all
+        if (warp == 0 && blockIdx.y == 0) {
+            if (p.sequences > (int)gridDim.x && lane == 0) p.joins[blockIdx.x] = make_int4(0, 0, 0, 0);
+            __syncwarp();
+            if (tiles > 0 && at >= first && at < last) write_join(p, ranges, lane, at, (int)tiles);
         }
+        start = Cursor{lane, (int)(first - at), (int)tiles, len};
         const int from = __ffs(__ballot_sync(0xFFFFFFFFu, holds)) - 1;
         start.b = __shfl_sync(0xFFFFFFFFu, start.b, from & 31);
         start.tile = __shfl_sync(0xFFFFFFFFu, start.tile, from & 31);
@@ -462,7 +446,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 const Batch next = lookup();
                 if (f.tokens > 0 && (uint32_t)f.page >= (uint32_t)p.n_pages) {
                     set_status(p.status, ST_INVALID_ARG);
-                    f.tokens = 0;
+                    f.page = f.tokens = 0;
                 }
                 const int row = f.page * p.page_size + f.offset;
 #pragma unroll 1

@@ -287,11 +287,12 @@ __global__ void k_kv_read(KvReadParams p);
 // (each row in more pieces).
 constexpr int kPagedUnitsCta = 4;
 constexpr int kPagedMaxStages = 8;
+constexpr int kPagedMaxHeads = 65535;        // of queries: no more CTAs over the units than a grid's second axis has
 constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
 constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
 struct PagedPlan {
     int units_head, units;                   // units of a KV head, of all
-    int heads_shift, subs_shift, parts_shift, tile_shift;
+    int heads_shift, subs_shift, parts_shift;
     int blocks, ranges;                      // CTAs over the units; ranges of the tile list
     int stages, stage_bytes, smem;
 };
@@ -303,7 +304,6 @@ inline PagedPlan paged_plan(int heads_q, int heads_kv, int dim) {
     n.heads_shift = 0;
     while ((2 << (n.heads_shift + n.subs_shift)) <= kPagedUnitsCta && heads_kv % (2 << n.heads_shift) == 0) ++n.heads_shift;
     n.parts_shift = 3 - n.subs_shift - n.heads_shift;
-    n.tile_shift = 4 + n.parts_shift;
     n.blocks = (heads_kv >> n.heads_shift) * (n.units_head >> n.subs_shift);
     const int ctas = dim == 256 ? 148 : 296;                          // one wave of 148 SMs
     n.ranges = ctas / n.blocks > 1 ? ctas / n.blocks : 1;
@@ -325,7 +325,7 @@ inline size_t paged_scratch_bytes(const PagedPlan &n, int dim) {
 // Codes as (byte of a head, row, head), boxes of one head's bytes x 16 rows x
 // the CTA's heads; scales as (byte of 16, row, group of 16 bytes).
 struct PagedMaps {
-    CUtensorMap kc, ks, vc, vs;      // in this order: indexed from the first
+    CUtensorMap kc, ks, vc, vs;
 };
 
 struct PagedAttnParams {

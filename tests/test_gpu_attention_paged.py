@@ -148,6 +148,30 @@ def test_many_sequences():
     assert torch.equal(R.bits(o), R.bits(again)) and torch.equal(lse, l2)      # the same bits every time
 
 
+@pytest.mark.parametrize("n,heads", [(31, 8), (32, 1), (32, 40), (33, 1), (33, 40)])
+def test_sequences_around_the_number_a_warp_schedules(n, heads):
+    """Up to 32 sequences each warp schedules for itself; 40 heads leave fewer
+    ranges (29) than sequences, so that the joins are by range."""
+    lens = [(7 * b * b + b) % 90 for b in range(n)]
+    cache = Cache(lens, heads, 128, 16, n + heads)
+    q = _query(n, heads * 3, 128, 33)
+    o, lse = cache.attend(q.to(DEV))
+    _check(cache, q, o, lse, 128 ** -0.5)
+
+
+@pytest.mark.parametrize("lens,heads,group,dim,page", [
+    ([9000, 0, 30], 2, 8, 128, 16), ([40, 3, 17, 160], 4, 20, 64, 10), ([700, 50], 1, 6, 256, 32)])
+def test_output_in_place_of_the_query(lens, heads, group, dim, page):
+    cache = Cache(lens, heads, dim, page, 34)
+    q = _query(len(lens), heads * group, dim, 35).to(DEV)
+    o, lse = cache.attend(q)
+    rows = torch.full((len(lens), heads * group + 2, dim), 7.0, dtype=torch.bfloat16, device=DEV)
+    for x in (q.clone(), rows[:, 1:-1].copy_(q)):
+        got, got_lse = cache.attend(x, out=x)
+        assert got is x and torch.equal(R.bits(x), R.bits(o)) and torch.equal(got_lse, lse)
+    assert (rows[:, 0] == 7).all() and (rows[:, -1] == 7).all()
+
+
 def test_matches_the_contiguous_read():
     """The identity table over one pool is nvfp4_attention_decode; both are
     within their bounds, so they differ by at most two BF16 roundings and the

@@ -130,7 +130,7 @@ def _pools(rows=64, cols=256, layout=1, p=16):
 
 
 def test_write_refusals(lib):
-    def call(k=16, kt=256, kh=128, v=16, vt=256, vh=128, n=4, h=2, d=128, slots=16, K=None, V=None,
+    def call(k=16, kt=256, kh=128, v=8192, vt=256, vh=128, n=4, h=2, d=128, slots=16, K=None, V=None,
              pos=16, tab=16, rows=10, r=128, inter=0, ws=16, wsn=256):
         return lib.nvfp4_kv_write(k, kt, kh, v, vt, vh, n, h, d, slots, K or _pools(), V or _pools(), pos,
                                   tab, rows, r, inter, ws, wsn, None)
@@ -149,7 +149,7 @@ def test_write_refusals(lib):
 
 
 def test_read_refusals(lib):
-    def call(K=None, V=None, slots=16, rows=8, k=16, ldk=256, v=16, ldv=256, ws=16, wsn=256):
+    def call(K=None, V=None, slots=16, rows=8, k=16, ldk=256, v=8192, ldv=256, ws=16, wsn=256):
         return lib.nvfp4_kv_read(K or _pools(), V or _pools(), slots, rows, k, ldk, v, ldv, ws, wsn, None)
 
     assert call() in DEVICE
@@ -158,13 +158,14 @@ def test_read_refusals(lib):
     assert call(k=24) == ALIGN and call(ldv=260) == ALIGN
     assert call(ldk=248) == SHAPE and call(K=_pools(layout=0)) == SHAPE and call(rows=2 ** 31) == SHAPE
     assert call(ws=0) == WS
+    assert call(v=16) == ARG                                # one output for both
 
 
 def test_attention_refusals(lib):
     big = 1 << 30
 
     def call(q=16, qb=512, qh=128, n=4, hq=4, K=None, V=None, hk=2, bt=16, bts=8, pages=8, lens=16, page=16,
-             scale=0.1, o=16, ob=512, oh=128, lse=16, ws=16, wsn=256, sc=16, scn=big):
+             scale=0.1, o=8192, ob=512, oh=128, lse=16, ws=16, wsn=256, sc=16, scn=big):
         return lib.nvfp4_attention_decode_paged(q, qb, qh, n, hq, K or _pools(), V or _pools(), hk, bt, bts,
                                                 pages, lens, page, scale, o, ob, oh, lse, ws, wsn, sc, scn, None)
 
@@ -182,6 +183,10 @@ def test_attention_refusals(lib):
     assert call(pages=0, bt=0) in DEVICE                                 # no pages: every sequence is empty
     assert call(q=24) == ALIGN and call(qb=516) == ALIGN and call(lens=18) == ALIGN and call(lse=18) == ALIGN
     assert call(ob=0) == SHAPE and call(oh=64) == SHAPE and call(qb=0, qh=0) in DEVICE
+    assert call(o=16) in DEVICE and call(n=1, o=16, ob=1024) in DEVICE   # in place
+    assert call(o=16, ob=1024) == ARG and call(o=16, oh=256, ob=1024) == ARG
+    assert call(hq=2 ** 16, qb=2 ** 23, ob=2 ** 23) == SHAPE
+    assert lib.nvfp4_attention_paged_scratch_bytes(2 ** 16, 1, 128) == 0
     assert call(wsn=10) == WS
     need = lib.nvfp4_attention_paged_scratch_bytes(4, 2, 128)
     if need:
