@@ -452,7 +452,7 @@ NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *
  *         they may not overlap in part.  head_dim = K->cols / heads_kv: 64,
  *         128, 256.  heads_q < 2^16.
  * page_size: any; K->rows a multiple of it and below 2^31.  table_pages *
- *   page_size < 2^31 - 1024, sequences * (table_pages * page_size / 16 + 1) < 2^31.
+ *   page_size < 2^31 - 1024, sequences * (table_pages * page_size / 16 + 8) < 2^31.
  * scratch: nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, head_dim)
  *   bytes, 16-byte aligned, of any content; calls that may run at the same
  *   time need scratch of their own (they may share the workspace, of which

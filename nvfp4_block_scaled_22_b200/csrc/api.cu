@@ -1031,8 +1031,8 @@ nvfp4_status nvfp4_attention_decode_paged(const void *q, int64_t q_seq_stride, i
     // token numbers, and those of a last tile's empty places, are counted in 31 bits
     if ((int64_t)table_pages * page_size > INT32_MAX - 1024) return NVFP4_ERR_SHAPE;
     if (sequences > 1 && table_stride < table_pages) return NVFP4_ERR_SHAPE;
-    // so are the 16-token tiles of all sequences
-    if ((int64_t)sequences * (1 + (int64_t)table_pages * page_size / 16) > INT32_MAX) return NVFP4_ERR_SHAPE;
+    // so are the 16-token tiles of all sequences and what the schedule adds to each
+    if ((int64_t)sequences * (8 + (int64_t)table_pages * page_size / 16) > INT32_MAX) return NVFP4_ERR_SHAPE;
     st = check_workspace(workspace, workspace_bytes, kStatusBytes);
     if (st != NVFP4_OK) return st;
     const PagedPlan plan = paged_plan(heads_q, heads_kv, (int)dim);
