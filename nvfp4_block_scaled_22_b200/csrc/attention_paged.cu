@@ -190,6 +190,7 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(src), "n"(kBytes) : "memory");
 }
+__device__ __forceinline__ void prefetch_l1(const void *a) { asm volatile("prefetch.global.L1 [%0];" :: "l"(a)); }
 // __syncwarp as a statement that the reads below cannot move across
 __device__ __forceinline__ void warp_sync() { asm volatile("bar.warp.sync 0xFFFFFFFF;" ::: "memory"); }
 
@@ -851,20 +852,26 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
         for (int j = 0; j < S::kSteps; ++j) mine[32 * j] = make_float4(oacc[j][0], oacc[j][1], oacc[j][2], oacc[j][3]);
         if (g == 0) ml[warp][c] = make_float4(mp[0], lsum[0], mp[1], lsum[1]);
+        int next_len = 0;
+        if (left > 0) {                                             // length and query of the next sequence on their way
+            next_len = length_of(p, b + 1);
+            if (g < heads)
+                prefetch_l1(p.q + (int64_t)(b + 1) * p.qs_b + (int64_t)(head0 + g) * p.qs_h + (kD == 256 ? 32 * c : (kD / 4) * c));
+        }
         const int step = kWarps >> kPartsShift;                    // warps between two parts of a unit
         unit_barrier(1 + unit_cta, 32 * tw);
         float M[2] = {kLowest, kLowest}, L[2] = {0.0f, 0.0f};
 #pragma unroll 1
-        for (int w = unit_cta; w < kWarps; w += step) {
-            const float4 v = ml[w][c];
-            M[0] = fmaxf(M[0], v.x);
-            M[1] = fmaxf(M[1], v.z);
+        for (int w = unit_cta; w < kWarps; w += 2 * step) {
+            const float4 v = ml[w][c], u = ml[w + step][c];
+            M[0] = fmaxf(M[0], fmaxf(v.x, u.x));
+            M[1] = fmaxf(M[1], fmaxf(v.z, u.z));
         }
 #pragma unroll 1
-        for (int w = unit_cta; w < kWarps; w += step) {
-            const float4 v = ml[w][c];
-            L[0] += v.y * exp2_fast(v.x - M[0]);
-            L[1] += v.w * exp2_fast(v.z - M[1]);
+        for (int w = unit_cta; w < kWarps; w += 2 * step) {
+            const float4 v = ml[w][c], u = ml[w + step][c];
+            L[0] += v.y * exp2_fast(v.x - M[0]) + u.y * exp2_fast(u.x - M[0]);
+            L[1] += v.w * exp2_fast(v.z - M[1]) + u.w * exp2_fast(u.z - M[1]);
         }
         const bool whole = ends && starts_here;
         float f[2] = {1.0f, 1.0f};
@@ -882,13 +889,15 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         for (int j = part; j < S::kSteps; j += tw) {
             float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 1
-            for (int w = unit_cta; w < kWarps; w += step) {
-                const float4 v = sums[w * (2 * kD) + 32 * j + lane], x = ml[w][c];
+            for (int w = unit_cta; w < kWarps; w += 2 * step) {
+                const float4 v = sums[w * (2 * kD) + 32 * j + lane], u = sums[(w + step) * (2 * kD) + 32 * j + lane];
+                const float4 x = ml[w][c], y = ml[w + step][c];
                 const float f0 = exp2_fast(x.x - M[0]), f1 = exp2_fast(x.z - M[1]);
-                r[0] += v.x * f0;
-                r[1] += v.y * f1;
-                r[2] += v.z * f0;
-                r[3] += v.w * f1;
+                const float g0 = exp2_fast(y.x - M[0]), g1 = exp2_fast(y.z - M[1]);
+                r[0] += v.x * f0 + u.x * g0;
+                r[1] += v.y * f1 + u.y * g1;
+                r[2] += v.z * f0 + u.z * g0;
+                r[3] += v.w * f1 + u.w * g1;
             }
             if (whole) {
                 if (h0) *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0], r[2] * f[0]);
@@ -910,7 +919,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         unit_barrier(1 + unit_cta, 32 * tw);
         if (left == 0) break;
         ++b;
-        in_seq = tiles_of(length_of(p, b), (4 + kPartsShift));
+        in_seq = tiles_of(next_len, (4 + kPartsShift));
         starts_here = true;
     }
 }
