@@ -5,24 +5,41 @@
 // block_table[b][t / page_size] * page_size + t % page_size.
 //
 // Each cache byte is read once (0.5625 bytes a value) and restored in
-// registers; the bound is that read, as long as a value costs no more than
-// about three instructions of a lane (148 SMs hold 79 values a ns each at the
-// measured copy rate).
+// registers.  Bound: the read, and close behind it the instructions that
+// restore and multiply -- a 16-token tile of 8 heads x 128 dims takes a warp
+// about 280, two of a lane's a value -- so that the long calls end between
+// the two: 64 sequences of 8192 tokens, 8 KV heads x 128, 64 query heads 116
+// us (5.0 TB/s, 0.77 of a copy); one of 131072 tokens 40.6 us (3.7 TB/s; each
+// further 131072 take 26 us, 5.8 TB/s, the rest is start, ending and join);
+// 96 of 256 to 8192 tokens 60 us (4.2 TB/s).  One of 1000 tokens takes 9.5
+// us, of one token 6: two launches and four dependent reads (length, page,
+// tile, parts).
 //
 // Units and warps.  A unit is a KV head with up to 8 of its query heads (the 8
-// columns of an MMA); larger groups are several units.  A CTA has 8 warps
-// over `units_cta` neighbouring units (so that it reads whole pieces of a
-// cache row) and 8 / units_cta warps share the tokens of one unit.  Every
-// warp runs on its own 16-token tiles through a ring of cp.async stages and
-// keeps its own online softmax; nothing in the loop waits for another warp.
+// columns of an MMA); larger groups are several units.  A CTA has 8 computing
+// warps over neighbouring units (so that it reads whole pieces of a cache
+// row), and the warps of a unit share its tokens, 16 each; every warp keeps
+// its own online softmax over its tiles.  Two CTAs an SM (heads of 256 values:
+// one): one CTA of 16 computing warps was 1.5 % faster on equal long
+// sequences and 5 to 30 % slower elsewhere, as a sequence's ending then
+// idles the SM.
+//
+// Copies.  Two further warps fill a ring of stages, in turn; full / empty
+// mbarriers, every wait bounded.  Where 16 tokens share a page and a row's
+// scales are whole 16-byte groups, a stage's parts are boxes of a 3-D tiled
+// TMA load (bytes of a head x 16 rows x heads), swizzled by it; else each
+// token's row is looked up and copied in 16-byte pieces by cp.async to the
+// same places.  Computing warps that refilled the ring themselves took 150 us
+// against 130 at 64 x 8192 (registers).
 //
 // Schedule.  The sequences' tiles (16 tokens times the warps of a unit; an
 // empty sequence counts one), each sequence's behind some that stand for the
 // cost of taking up a sequence, are one list, cut into equal ranges, one a
 // CTA, on the device from seq_lens: the CTAs have equal work whatever the
-// lengths, and the host needs no length.  A sequence that ends
-// inside of its CTA's range is written at once; one that is cut leaves a
-// partial (m, l, O) per CTA, which k_paged_combine joins in CTA order.
+// lengths, and the host needs no length.  A sequence that ends inside of its
+// CTA's range is written at once; one that is cut leaves a partial (m, l, O)
+// per CTA, which k_paged_combine joins in the order of the ranges: the result
+// does not depend on which CTA ends first.
 //
 // A 16-token tile of a unit:
 //   S[16 tokens x 8 heads] = K q^T, mma.sync m16n8k16, FP16 operands, FP32
@@ -39,10 +56,11 @@
 //   O^T[dim x 8 heads] += V^T P^T, the same MMA: P goes from accumulator to
 //     operand layout by movmatrix; the codes of two tokens are interleaved
 //     by nibbles so that one conversion gives the two tokens of one dim.
-//   Token r of an MMA is token tau(r) of the tile (r = 8h + 2c + j: tau = 8h
-//   + 4j + (c ^ 3j)), and 16-byte pieces are stored xor-swizzled, so that
-//   both the row-wise reads of K and the column-wise reads of V meet no
-//   shared-memory bank twice.
+//   The rows of an MMA are the tile's tokens in an order (token_of) in which,
+//   under the copies' swizzle, neither the row-wise reads of K nor the
+//   column-wise reads of V meet a shared-memory bank twice.
+//   The query's fragments lie in shared memory, where the warp's O goes at
+//   the end: registers (96 at two CTAs) are what limits the warps of an SM.
 #include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
