@@ -393,11 +393,11 @@ NVFP4_API nvfp4_status nvfp4_rope_table(const double *d_inv_freq, int32_t rotary
  * x, y: BF16 [tokens][heads][head_dim], innermost contiguous, strides in
  *   elements (x may repeat rows by a stride of 0; y's rows may not overlap).
  *   y == x with equal strides works in place; they may not overlap in part.
- *   2-byte aligned; 16-byte aligned pieces (strides % 8 == 0, rotary_dim % 16
- *   == 0, or % 8 if interleaved) take the vectorised path.
+ *   2-byte aligned; 16-byte aligned with strides and head_dim % 8 == 0 is
+ *   vectorised (but for the half layout in place with rotary_dim % 16 != 0).
  * d_positions: int32[tokens]; position -1 leaves the token's y as it was.
  * rotary_dim: even, 2 .. head_dim.  tokens * heads * head_dim < 2^31 always
- *   fits (more does on the vectorised path; else NVFP4_ERR_SHAPE). */
+ *   fits (more does where vectorised; else NVFP4_ERR_SHAPE). */
 NVFP4_API nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride,
                                   int64_t tokens, int32_t heads, int32_t head_dim,
                                   const int32_t *d_positions, const float *d_table,

@@ -846,15 +846,20 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
                      (heads > 1 && x_head_stride != y_head_stride)))
         return NVFP4_ERR_INVALID_ARG;
     const int32_t pairs = rotary_dim / 2, rest = in_place ? 0 : head_dim - rotary_dim;
-    const bool pieces = aligned16(x) && aligned16(y) &&
-                        (x_token_stride | x_head_stride | y_token_stride | y_head_stride) % 8 == 0 &&
-                        rest % 8 == 0 && (interleaved ? pairs % 4 == 0 : pairs % 8 == 0);
-    const int64_t per_head = !pieces ? pairs + rest
-                                     : (interleaved ? (rotary_dim + rest) / 8 : pairs / 8 + rest / 8);
-    const bool by_groups = pieces && !interleaved;
-    const int64_t groups = by_groups ? ceil_div(heads, kRopeHeads) : heads;
+    const bool aligned = aligned16(x) && aligned16(y) &&
+                         (x_token_stride | x_head_stride | y_token_stride | y_head_stride) % 8 == 0;
+    // whole: the rotated part and the rest come out in whole pieces; else pieces that their borders cut
+    const bool whole = aligned && rest % 8 == 0 && (interleaved ? pairs % 4 == 0 : pairs % 8 == 0);
+    const bool pieces = whole || (aligned && head_dim % 8 == 0 && (interleaved || !in_place));
+    const int64_t per_head = !pieces       ? pairs + rest
+                             : interleaved ? (in_place ? ceil_div(rotary_dim, 8) : head_dim / 8)
+                             : whole       ? (pairs + rest) / 8
+                                           : head_dim / 8;
+    const int64_t groups = pieces && !interleaved ? ceil_div(heads, kRopeHeads) : heads;
+    // pieces that a border of the rotated part cuts, for which k_rope_half_pieces has items of their own
+    const int cuts = !pieces || whole || interleaved ? 0 : pairs % 4 == 0 || pairs < 4 ? 1 : 2;
     // items are counted in 31 bits
-    if (tokens > INT32_MAX / per_head / groups) return NVFP4_ERR_SHAPE;
+    if (tokens > INT32_MAX / (per_head + cuts) / groups) return NVFP4_ERR_SHAPE;
     int sms = 0;
     st = current_device(&sms);
     if (st != NVFP4_OK) return st;
@@ -871,17 +876,23 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
     p.pairs = pairs;
     p.heads = heads;
     p.sign = inverse ? -1.0f : 1.0f;
-    p.items = (uint32_t)(tokens * groups * per_head);
-    p.per_token = fast_div((uint32_t)(groups * per_head));
+    p.uncut = (uint32_t)(groups * per_head);
+    p.cuts = (uint32_t)cuts;
+    p.items = (uint32_t)(tokens * groups * (per_head + cuts));
+    p.per_token = fast_div((uint32_t)(groups * (per_head + cuts)));
     p.per_head = fast_div((uint32_t)per_head);
     p.status = static_cast<uint32_t *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!pieces)
         k_rope_any<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p, interleaved, rest > 0);
-    else if (interleaved)
+    else if (interleaved && whole)
         k_rope_interleaved<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
-    else
+    else if (interleaved)
+        k_rope_interleaved_pieces<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+    else if (whole)
         k_rope_half<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p);
+    else
+        k_rope_half_pieces<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p);
     return launched(cudaGetLastError());
 }
 

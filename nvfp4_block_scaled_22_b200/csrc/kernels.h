@@ -223,6 +223,9 @@ struct RopeParams {
     float sign;              // +1, or -1 for the inverse
     uint32_t items;          // work items (tokens x heads x items of a head)
     FastDiv per_token, per_head;
+    // half layout in pieces that the rotated part's borders cut: a token's
+    // items but for those of the cut pieces, and cut pieces of a head (1 or 2)
+    uint32_t uncut, cuts;
     uint32_t *status;
 };
 constexpr int kRopeItems = 2;   // interleaved layout: items a thread takes, 256 apart
@@ -230,7 +233,9 @@ constexpr int kRopeHeads = 4;   // half layout: heads an item takes
 __global__ void k_rope_table(const double *inv_freq, int32_t pairs, int64_t first, int64_t n,
                              double magnitude, float2 *table);
 __global__ void k_rope_half(RopeParams p);
+__global__ void k_rope_half_pieces(RopeParams p);
 __global__ void k_rope_interleaved(RopeParams p);
+__global__ void k_rope_interleaved_pieces(RopeParams p);
 __global__ void k_rope_any(RopeParams p, int interleaved, int with_rest);
 
 // Paged cache write and read (kv_cache.cu).

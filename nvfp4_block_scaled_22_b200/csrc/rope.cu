@@ -12,7 +12,8 @@
 // reduced to a turn, so an FP32 angle is off by 0.06 at position 2^20.
 //
 // Bound by memory: 4 bytes a value against 3 FP32 operations (8192 x 72 x 128
-// in 47.8 us, 6.4 TB/s; 4099 x 40 x 128 interleaved, half rotated, in 13.9 us).
+// in 47.5 us, 6.4 TB/s; interleaved 51.4; 4099 x 40 x 128 interleaved, half
+// rotated, in 15.7 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -115,8 +116,124 @@ __global__ void __launch_bounds__(256) k_rope_half(RopeParams p) {
     }
 }
 
-// Interleaved layout, 8 values (4 pairs) an item.
-__global__ void __launch_bounds__(256) k_rope_interleaved(RopeParams p) {
+// Values o .. o + 7 of the two 16-byte pieces (a, b), in bits.
+__device__ __forceinline__ uint4 window(const uint4 &a, const uint4 &b, uint32_t o) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (o & 4u) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (o & 2u) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (o & 1u) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Half layout with any pair count, y apart from x: an item is a 16-byte piece
+// of kRopeHeads heads of the output, whose partners lie in two neighbouring
+// pieces of x; each value is rotated by itself, x c + partner (-s, or s in
+// the second half), the same steps.  The pieces that a border of the rotated
+// part cuts go value by value, as items behind a token's others: among them,
+// each warp had waited for a few such lanes (8192 x 72 x 128 with 63 pairs: 175
+// us, so 95; with 31 pairs 85, with one 55; pair by pair in k_rope_any 177, 260
+// and 306.  8 heads an item, fewer warps: 138 with 63 pairs).
+__global__ void __launch_bounds__(256) k_rope_half_pieces(RopeParams p) {
+    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    if (item >= p.items) return;
+    const uint32_t pairs = (uint32_t)p.pairs;
+    const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
+    const bool cut = in_t >= p.uncut;
+    const uint32_t border = (in_t - p.uncut) & (p.cuts - 1);            // of a cut item
+    const uint32_t group = cut ? (in_t - p.uncut) >> (p.cuts - 1) : quotient(in_t, p.per_head);
+    // the borders are at pairs (pairs % 8 != 0 here) and 2 * pairs (in the same piece, or between two, with one cut)
+    const uint32_t at = cut ? ((border == 0u ? pairs : 2 * pairs) & ~7u) : 8 * (in_t - group * p.per_head.d);
+    const bool first = at + 8 <= pairs, second = at >= pairs && at + 8 <= 2 * pairs;
+    if (!cut && !first && !second && at < 2 * pairs) return;
+    const int h0 = (int)group * kRopeHeads;
+    const uint16_t *x = p.x + (int64_t)t * p.xs_t + (int64_t)h0 * p.xs_h;
+    uint16_t *y = p.y + (int64_t)t * p.ys_t + (int64_t)h0 * p.ys_h + at;
+    const int64_t row = rope_row(p.positions[t], p.table_rows, p.status);
+    if (row < 0) return;
+    const float2 *table = p.table + row * pairs;
+    uint4 a[kRopeHeads];
+#pragma unroll
+    for (int h = 0; h < kRopeHeads; ++h)
+        a[h] = h0 + h < p.heads ? __ldg(reinterpret_cast<const uint4 *>(x + (int64_t)h * p.xs_h + at)) : make_uint4(0u, 0u, 0u, 0u);
+    if (!cut && (first || second)) {
+        const uint32_t from = first ? at + pairs : at - pairs, o = from & 7u;
+        uint4 b[kRopeHeads];
+#pragma unroll
+        for (int h = 0; h < kRopeHeads; ++h) {
+            if (h0 + h < p.heads) {
+                const uint4 *q = reinterpret_cast<const uint4 *>(x + (int64_t)h * p.xs_h + (from - o));
+                const uint4 b0 = __ldg(q);
+                b[h] = o != 0u ? window(b0, __ldg(q + 1), o) : b0;
+            }
+        }
+        const float2 *cs = table + (first ? at : at - pairs);
+        const float sign = first ? -p.sign : p.sign;
+        float2 f[8];
+        if ((pairs & 1u) == 0u) {                       // 16-byte aligned rows, and half of the loads
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float4 two = __ldg(reinterpret_cast<const float4 *>(cs) + i);
+                f[2 * i] = make_float2(two.x, two.y);
+                f[2 * i + 1] = make_float2(two.z, two.w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __ldg(cs + i);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i].y *= sign;
+#pragma unroll
+        for (int h = 0; h < kRopeHeads; ++h) {
+            if (h0 + h < p.heads) {
+                const uint32_t aw[4] = {a[h].x, a[h].y, a[h].z, a[h].w}, bw[4] = {b[h].x, b[h].y, b[h].z, b[h].w};
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = bf16x2_from_f32(
+                        __fadd_rn(__fmul_rn(bf16_lo(aw[i]), f[2 * i].x), __fmul_rn(bf16_lo(bw[i]), f[2 * i].y)),
+                        __fadd_rn(__fmul_rn(bf16_hi(aw[i]), f[2 * i + 1].x), __fmul_rn(bf16_hi(bw[i]), f[2 * i + 1].y)));
+                a[h] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    } else if (cut) {
+#pragma unroll
+        for (uint32_t n = 0; n < 8; ++n) {
+            const uint32_t i = at + n;
+            if (i < 2 * pairs) {
+                const uint32_t other = i < pairs ? i + pairs : i - pairs;
+                const float2 f = __ldg(table + min(i, other));
+                const float s = i < pairs ? -p.sign * f.y : p.sign * f.y;
+#pragma unroll
+                for (int h = 0; h < kRopeHeads; ++h) {
+                    if (h0 + h < p.heads) {
+                        uint32_t w[4] = {a[h].x, a[h].y, a[h].z, a[h].w};
+                        const float v = (n & 1u) ? bf16_hi(w[n >> 1]) : bf16_lo(w[n >> 1]);
+                        const float r = __fadd_rn(__fmul_rn(v, f.x), __fmul_rn(bf16_lo(__ldg(x + (int64_t)h * p.xs_h + other)), s));
+                        const uint32_t bits = bf16x2_from_f32(r, r);
+                        w[n >> 1] = (n & 1u) ? (w[n >> 1] & 0xFFFFu) | (bits & 0xFFFF0000u) : (w[n >> 1] & 0xFFFF0000u) | (bits & 0xFFFFu);
+                        a[h] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < kRopeHeads; ++h)
+        if (h0 + h < p.heads) *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h) = a[h];
+}
+
+// Interleaved layout, 8 values (4 pairs) an item; kWhole: pairs % 4 == 0.
+template <bool kWhole>
+__device__ __forceinline__ void rope_interleaved(const RopeParams &p) {
     const uint32_t base = blockIdx.x * (256u * kRopeItems) + threadIdx.x;
     RopeItem it[kRopeItems];
     uint4 a[kRopeItems];
@@ -130,26 +247,37 @@ __global__ void __launch_bounds__(256) k_rope_interleaved(RopeParams p) {
     for (int n = 0; n < kRopeItems; ++n) {
         if (it[n].row < 0) continue;
         uint4 y = a[n];
-        if (4 * it[n].piece < (uint32_t)p.pairs) {
-            const float4 *cs = reinterpret_cast<const float4 *>(p.table + it[n].row * p.pairs + 4 * it[n].piece);
-            const float4 f0 = __ldg(cs), f1 = __ldg(cs + 1);
-            float lo, hi;
-            rotate(bf16_lo(a[n].x), bf16_hi(a[n].x), f0.x, p.sign * f0.y, lo, hi);
-            y.x = bf16x2_from_f32(lo, hi);
-            rotate(bf16_lo(a[n].y), bf16_hi(a[n].y), f0.z, p.sign * f0.w, lo, hi);
-            y.y = bf16x2_from_f32(lo, hi);
-            rotate(bf16_lo(a[n].z), bf16_hi(a[n].z), f1.x, p.sign * f1.y, lo, hi);
-            y.z = bf16x2_from_f32(lo, hi);
-            rotate(bf16_lo(a[n].w), bf16_hi(a[n].w), f1.z, p.sign * f1.w, lo, hi);
-            y.w = bf16x2_from_f32(lo, hi);
+        const uint32_t pair = 4 * it[n].piece;
+        if (pair < (uint32_t)p.pairs) {
+            const float2 *cs = p.table + it[n].row * p.pairs + pair;
+            float2 f[4];
+            if (kWhole) {
+                const float4 f0 = __ldg(reinterpret_cast<const float4 *>(cs)), f1 = __ldg(reinterpret_cast<const float4 *>(cs) + 1);
+                f[0] = make_float2(f0.x, f0.y), f[1] = make_float2(f0.z, f0.w);
+                f[2] = make_float2(f1.x, f1.y), f[3] = make_float2(f1.z, f1.w);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = pair + i < (uint32_t)p.pairs ? __ldg(cs + i) : make_float2(0.0f, 0.0f);
+            }
+            uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float lo, hi;
+                rotate(bf16_lo(w[i]), bf16_hi(w[i]), f[i].x, p.sign * f[i].y, lo, hi);
+                if (kWhole || pair + i < (uint32_t)p.pairs) w[i] = bf16x2_from_f32(lo, hi);
+            }
+            y = make_uint4(w[0], w[1], w[2], w[3]);
         }
         *reinterpret_cast<uint4 *>(it[n].y + 8 * it[n].piece) = y;
     }
 }
+__global__ void __launch_bounds__(256) k_rope_interleaved(RopeParams p) { rope_interleaved<true>(p); }
+__global__ void __launch_bounds__(256) k_rope_interleaved_pieces(RopeParams p) { rope_interleaved<false>(p); }
 
 // Any pair count, head size and alignment: one pair an item, then one value
-// an item behind the rotated part.  Taken where the pieces above do not come
-// out whole or 16-byte aligned.
+// an item behind the rotated part.  Taken where heads are not 16-byte aligned
+// pieces, and for the half layout in place with pairs % 8 != 0 (the pieces'
+// partners would have been overwritten).
 __global__ void __launch_bounds__(256) k_rope_any(RopeParams p, int interleaved, int with_rest) {
     const uint32_t item = blockIdx.x * 256u + threadIdx.x;
     if (item >= p.items) return;

@@ -64,6 +64,29 @@ def test_rotation_matches_formula_and_steps(tokens, heads, dim, rotary, interlea
     assert np.all(np.abs(R.f64(y) - exact) <= 2.0 ** -8 * (np.abs(exact) + slack) + slack)
 
 
+@pytest.mark.parametrize("tokens,heads,dim,rotary", [
+    (9, 5, 128, 2), (7, 6, 64, 54), (5, 9, 256, 206), (6, 1, 72, 38), (300, 3, 128, 30), (2, 4, 8, 2), (3, 5, 16, 14),
+    (4, 8, 128, 126), (8, 2, 24, 20), (2, 3, 8, 8), (5, 7, 256, 250)])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_pair_counts_that_cut_a_piece(tokens, heads, dim, rotary, interleaved):
+    """Rotated parts that end inside of 16 bytes: apart, inverse, in place,
+    head-major, and with what is not finite kept to its pair."""
+    x, pos, table = _case(tokens, heads, dim, rotary, dim + rotary, far=4096)
+    x[0, 0, dim - 1], x[-1, -1, 0] = float("nan"), float("inf")
+    want = _same_steps(x, pos, table, interleaved)
+
+    def same(got, want):
+        nan = torch.isnan(want.float())
+        return torch.equal(torch.isnan(got.float()), nan) and torch.equal(R.bits(got)[~nan], R.bits(want)[~nan])
+
+    d = x.to(DEV)
+    assert same(nb.nvfp4_rope(d, pos.to(DEV), table, interleaved).cpu(), want)
+    assert same(nb.nvfp4_rope(d, pos.to(DEV), table, interleaved, inverse=True).cpu(), _same_steps(x, pos, table, interleaved, True))
+    flip = torch.empty(heads, tokens, dim, dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    assert same(nb.nvfp4_rope(d, pos.to(DEV), table, interleaved, out=flip).cpu(), want)
+    assert same(nb.nvfp4_rope(d, pos.to(DEV), table, interleaved, out=d).cpu(), want)
+
+
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_inverse_is_the_gradient(interleaved):
     """<R x, g> = <x, R^T g>, against differences of the formula as well."""
