@@ -15,7 +15,7 @@
 //
 // Both are bound by memory (2.56 bytes a value): 131072 rows of 2 x 1024
 // values are read back in 108 us (6.4 TB/s), 16384 tokens of 2 x 8 x 128
-// written in 17.9 us (4.8 TB/s, launch included), with rotated keys in 24.7
+// written in 17.7 us (4.9 TB/s, launch included), with rotated keys in 23.9
 // us -- a key block then costs 12 instructions a value, on loads that wait
 // for the position and then for the table row.  Tried for the write: a half
 // block a thread (30 us: the scale's arithmetic twice), two heads a thread
@@ -65,7 +65,8 @@ __device__ __forceinline__ void rotate_blocks(Block &a, Block &b, const float2 *
 }
 
 // Block `blk` of head x rotated by itself: neighbouring pairs, or partners
-// fetched one by one (any pair count).
+// fetched by 8 (pairs % 8 == 0: 16384 x 16 x 64 with 8 pairs in 24.9 us, one by
+// one 35.7) or one by one (any pair count).
 __device__ __forceinline__ void rotate_alone(Block &a, const uint16_t *x, int blk, const KvWriteParams &p,
                                              int64_t pos) {
     const int j0 = 16 * blk;
@@ -81,6 +82,27 @@ __device__ __forceinline__ void rotate_alone(Block &a, const uint16_t *x, int bl
                 float y1, y2;
                 rotate(bf16_lo(w[i]), bf16_hi(w[i]), f.x, f.y, y1, y2);
                 w[i] = bf16x2_from_f32(y1, y2);
+            }
+        }
+    } else if (p.pairs % 8 == 0) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j = j0 + 8 * n;
+            if (j < 2 * p.pairs) {
+                const bool first = j < p.pairs;
+                const int pair = first ? j : j - p.pairs;
+                const uint4 q = *reinterpret_cast<const uint4 *>(first ? x + j + p.pairs : x + pair);
+                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+                const float4 *cs = reinterpret_cast<const float4 *>(row + pair);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 f = __ldg(cs + i);
+                    const uint32_t a1 = first ? w[4 * n + i] : u[i], a2 = first ? u[i] : w[4 * n + i];
+                    float lo1, lo2, hi1, hi2;
+                    rotate(bf16_lo(a1), bf16_lo(a2), f.x, f.y, lo1, lo2);
+                    rotate(bf16_hi(a1), bf16_hi(a2), f.z, f.w, hi1, hi2);
+                    w[4 * n + i] = first ? bf16x2_from_f32(lo1, hi1) : bf16x2_from_f32(lo2, hi2);
+                }
             }
         }
     } else {
