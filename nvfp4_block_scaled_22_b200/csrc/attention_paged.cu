@@ -536,7 +536,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             const int tokens_stage = kTile << kPartsShift;
             int *rows = rows_sh[warp - kWarps];
             const int piece_shift = plan.heads_shift + (kD == 64 ? 1 : kD == 128 ? 2 : 3);
-            const int scales_from = (head_first * S::kScales) & ~15;
+            // a lane's place in the rows' pieces and scales, the same in every step (both are at most 32 a token)
+            const int x = lane & ((1 << piece_shift) - 1), h = lane & (heads_cta - 1);
+            const uint8_t *kc = p.kc + (int64_t)head_first * S::kCodes + 16 * x, *vc = p.vc + (int64_t)head_first * S::kCodes + 16 * x;
+            const int byte = (head_first + h) * S::kScales;             // of a row's scales
+            const uint32_t codes_at = (uint32_t)(x / S::kChunks) * (kTile * S::kCodes);
+            const uint32_t scales_at = k_scales + (uint32_t)((byte - ((head_first * S::kScales) & ~15)) >> 4) * (16 * kTile) + (byte & 15);
             int pages[4], offsets[4];                                   // tokens lane, lane + 32, ...
             auto lookup = [&]() {
 #pragma unroll
@@ -582,30 +587,23 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 lookup();
                 __syncwarp();
                 const uint32_t to = ring + stage * plan.stage_bytes;
-#pragma unroll 2
-                for (int n = lane; n < tokens_stage << piece_shift; n += 32) {
-                    const int t = n >> piece_shift, x = n & ((1 << piece_shift) - 1);
-                    const int h = x / S::kChunks, ch = x % S::kChunks;
+#pragma unroll 4
+                for (int t = lane >> piece_shift; t < tokens_stage; t += 32 >> piece_shift) {
                     const int r = rows[t];
+                    const uint32_t dst = to + codes_at + ((t >> 4) << plan.heads_shift) * (kTile * S::kCodes) +
+                                         (t & 15) * S::kCodes + 16 * swizzled<kD>(x % S::kChunks, t & 15);
                     if (r >= 0) {
-                        const int64_t src = (int64_t)r * p.row_codes + (int64_t)(head_first + h) * S::kCodes + 16 * ch;
-                        const uint32_t dst = to + (((t >> 4) << plan.heads_shift) + h) * (kTile * S::kCodes) +
-                                             (t & 15) * S::kCodes + 16 * swizzled<kD>(ch, t & 15);
-                        copy_async<16>(dst, p.kc + src);
-                        copy_async<16>(dst + v_codes, p.vc + src);
+                        copy_async<16>(dst, kc + (int64_t)r * p.row_codes);
+                        copy_async<16>(dst + v_codes, vc + (int64_t)r * p.row_codes);
                     }
                 }
-#pragma unroll 2
-                for (int n = lane; n < tokens_stage << plan.heads_shift; n += 32) {
-                    const int t = n >> plan.heads_shift, h = n & (heads_cta - 1);
+#pragma unroll 4
+                for (int t = lane >> plan.heads_shift; t < tokens_stage; t += 32 >> plan.heads_shift) {
                     const int r = rows[t];
+                    const uint32_t dst = to + scales_at + (t >> 4) * scale_groups * (16 * kTile) + (t & 15) * 16;
                     if (r >= 0) {
-                        const int x = (head_first + h) * S::kScales;    // byte of the row
-                        const int64_t src = (int64_t)r * p.row_scales + x;
-                        const uint32_t dst = to + k_scales + ((t >> 4) * scale_groups + ((x - scales_from) >> 4)) * (16 * kTile) +
-                                             (t & 15) * 16 + (x & 15);
-                        copy_async<S::kScales>(dst, p.ks + src);
-                        copy_async<S::kScales>(dst + (v_scales - k_scales), p.vs + src);
+                        copy_async<S::kScales>(dst, p.ks + (int64_t)r * p.row_scales + byte);
+                        copy_async<S::kScales>(dst + (v_scales - k_scales), p.vs + (int64_t)r * p.row_scales + byte);
                     }
                 }
                 copies_arrive(&full[stage]);
