@@ -24,12 +24,13 @@
 // sequences and 5 to 30 % slower elsewhere, as a sequence's ending then
 // idles the SM.
 //
-// Copies.  Two further warps fill a ring of stages, in turn; full / empty
+// Copies.  Two (or four) further warps fill a ring of stages, in turn; full / empty
 // mbarriers, every wait bounded.  Where 16 tokens share a page and a row's
 // scales are whole 16-byte groups, a stage's parts are boxes of a 3-D tiled
 // TMA load (bytes of a head x 16 rows x heads), swizzled by it; else each
 // token's row is looked up and copied in 16-byte pieces by cp.async to the
-// same places.  Computing warps that refilled the ring themselves took 150 us
+// same places (pages of 20 tokens: 64 x 8192 in 171 us, bound by the copying
+// warps' instructions).  Computing warps that refilled the ring themselves took 150 us
 // against 130 at 64 x 8192 (registers).
 //
 // Schedule.  The sequences' tiles (16 tokens times the warps of a unit; an
@@ -80,8 +81,14 @@ constexpr float kOffset = 6.0f;      // m' is this much below the reference
 constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' moves
 
 constexpr int kWarps = 8;            // warps that compute
-constexpr int kProducers = 2;       // warps that bring the tiles in, stages in turn
-constexpr int kThreads = 32 * (kWarps + kProducers);
+// Warps that bring the tiles in, stages in turn.  Copies by cp.async take four
+// where the registers of two further warps are free (4 x 3 .. 97886 tokens, 5
+// heads x 64: 50.1 -> 42.8 us; 112 x 270 .. 574, 5 x 256: 43.6 -> 41.1; with
+// heads of 128 values 80 registers spill: 64 x 8192 in pages of 20 171 -> 179).
+template <int kD, bool kTma>
+struct Producers {
+    static constexpr int kCount = kTma || kD == 128 ? 2 : 4;
+};
 constexpr long long kDrainCycles = 2000000000ll;   // bound of the wait for copies under way (about a second)
 constexpr int kTile = 16;            // tokens of a warp's tile
 
@@ -300,9 +307,10 @@ struct Cursor {
 }  // namespace
 
 template <int kD, bool kTma, int kPartsShift>
-__global__ void __launch_bounds__(kThreads, Shape<kD>::kCtasPerSm)
+__global__ void __launch_bounds__(32 * (kWarps + Producers<kD, kTma>::kCount), Shape<kD>::kCtasPerSm)
 k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_constant__ PagedMaps maps) {
     using S = Shape<kD>;
+    constexpr int kProducers = Producers<kD, kTma>::kCount, kThreads = 32 * (kWarps + kProducers);
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
     __shared__ int masks[kPagedMaxStages][kWarps];
@@ -1060,6 +1068,9 @@ cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t 
 
 template <int kD, bool kTma, int kPartsShift>
 cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
+    constexpr int kProducers = Producers<kD, kTma>::kCount;
+    // a producer that is not a stage behind itself could mistake a barrier's phase
+    if (p.plan.stages < kProducers) return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> ready{0};               // devices (below 64) with the shared memory allowed
     const void *kernel = (const void *)k_paged_attention<kD, kTma, kPartsShift>;
     int dev = 0;
@@ -1072,7 +1083,7 @@ cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStr
         ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
     void *args[] = {const_cast<PagedAttnParams *>(&p), const_cast<PagedMaps *>(&maps)};
-    return launch_dependent(kernel, dim3((unsigned)p.plan.ranges, (unsigned)p.plan.blocks), kThreads,
+    return launch_dependent(kernel, dim3((unsigned)p.plan.ranges, (unsigned)p.plan.blocks), 32 * (kWarps + kProducers),
                             (size_t)p.plan.smem, s, args);
 }
 

@@ -294,7 +294,7 @@ constexpr int kPagedUnitsCta = 4;
 constexpr int kPagedMaxStages = 8;
 constexpr int kPagedMaxHeads = 65535;        // of queries: no more CTAs over the units than a grid's second axis has
 constexpr int kPagedSmem = 112 * 1024;       // two CTAs an SM
-constexpr int kPagedSmem256 = 224 * 1024;    // one CTA an SM
+constexpr int kPagedSmem256 = 223 * 1024;    // one CTA an SM, with some 3 KB of barriers and the like
 struct PagedPlan {
     int units_head, units;                   // units of a KV head, of all
     int heads_shift, subs_shift, parts_shift;
