@@ -855,7 +855,7 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
                              : interleaved ? (in_place ? ceil_div(rotary_dim, 8) : head_dim / 8)
                              : whole       ? (pairs + rest) / 8
                                            : head_dim / 8;
-    const int64_t groups = pieces && !interleaved ? ceil_div(heads, kRopeHeads) : heads;
+    const int64_t groups = pieces ? ceil_div(heads, kRopeHeads) : heads;
     // pieces that a border of the rotated part cuts, for which k_rope_half_pieces has items of their own
     const int cuts = !pieces || whole || interleaved ? 0 : pairs % 4 == 0 || pairs < 4 ? 1 : 2;
     // items are counted in 31 bits
@@ -883,16 +883,17 @@ nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t x_head_st
     p.per_head = fast_div((uint32_t)per_head);
     p.status = static_cast<uint32_t *>(workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)ceil_div(p.items, 256);
     if (!pieces)
-        k_rope_any<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p, interleaved, rest > 0);
+        k_rope_any<<<grid, 256, 0, s>>>(p, interleaved, rest > 0);
     else if (interleaved && whole)
-        k_rope_interleaved<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+        k_rope_interleaved<<<grid, 256, 0, s>>>(p);
     else if (interleaved)
-        k_rope_interleaved_pieces<<<(unsigned)ceil_div(p.items, 256 * kRopeItems), 256, 0, s>>>(p);
+        k_rope_interleaved_pieces<<<grid, 256, 0, s>>>(p);
     else if (whole)
-        k_rope_half<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p);
+        k_rope_half<<<grid, 256, 0, s>>>(p);
     else
-        k_rope_half_pieces<<<(unsigned)ceil_div(p.items, 256), 256, 0, s>>>(p);
+        k_rope_half_pieces<<<grid, 256, 0, s>>>(p);
     return launched(cudaGetLastError());
 }
 

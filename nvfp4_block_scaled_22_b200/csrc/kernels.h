@@ -228,8 +228,7 @@ struct RopeParams {
     uint32_t uncut, cuts;
     uint32_t *status;
 };
-constexpr int kRopeItems = 2;   // interleaved layout: items a thread takes, 256 apart
-constexpr int kRopeHeads = 4;   // half layout: heads an item takes
+constexpr int kRopeHeads = 4;   // heads that an item of 16-byte pieces takes
 __global__ void k_rope_table(const double *inv_freq, int32_t pairs, int64_t first, int64_t n,
                              double magnitude, float2 *table);
 __global__ void k_rope_half(RopeParams p);

@@ -12,8 +12,8 @@
 // reduced to a turn, so an FP32 angle is off by 0.06 at position 2^20.
 //
 // Bound by memory: 4 bytes a value against 3 FP32 operations (8192 x 72 x 128
-// in 47.5 us, 6.4 TB/s; interleaved 51.4; 4099 x 40 x 128 interleaved, half
-// rotated, in 15.7 us).
+// in 47.5 us, 6.4 TB/s; interleaved 46.4; 4099 x 40 x 128 interleaved, half
+// rotated, in 14.9 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -32,26 +32,6 @@ __global__ void __launch_bounds__(256) k_rope_table(const double *__restrict__ i
         sincos((double)(first + row) * inv_freq[e - row * pairs], &s, &c);
         table[e] = make_float2((float)(c * magnitude), (float)(s * magnitude));
     }
-}
-
-// Where an item lies: a token's position row (-1: left alone), and the item's
-// piece of a head.
-struct RopeItem {
-    int64_t row;
-    const uint16_t *x;
-    uint16_t *y;
-    uint32_t piece;
-};
-
-__device__ __forceinline__ RopeItem rope_item(const RopeParams &p, uint32_t item) {
-    const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
-    const uint32_t h = quotient(in_t, p.per_head);
-    RopeItem r;
-    r.row = rope_row(p.positions[t], p.table_rows, p.status);
-    r.x = p.x + (int64_t)t * p.xs_t + (int64_t)h * p.xs_h;
-    r.y = p.y + (int64_t)t * p.ys_t + (int64_t)h * p.ys_h;
-    r.piece = in_t - h * p.per_head.d;
-    return r;
 }
 
 // Half layout: an item is 8 pairs (two 16-byte pieces) of kRopeHeads heads
@@ -231,44 +211,52 @@ __global__ void __launch_bounds__(256) k_rope_half_pieces(RopeParams p) {
         if (h0 + h < p.heads) *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h) = a[h];
 }
 
-// Interleaved layout, 8 values (4 pairs) an item; kWhole: pairs % 4 == 0.
+// Interleaved layout: an item is 8 values (4 pairs) of kRopeHeads heads of a
+// token, which share 32 bytes of the table; kWhole: pairs % 4 == 0.  (An item
+// a head took the table once a head: 8192 x 72 x 128 in 51.0 us, so 46.4; with
+// 63 pairs 59.5 and 47.3.)
 template <bool kWhole>
 __device__ __forceinline__ void rope_interleaved(const RopeParams &p) {
-    const uint32_t base = blockIdx.x * (256u * kRopeItems) + threadIdx.x;
-    RopeItem it[kRopeItems];
-    uint4 a[kRopeItems];
+    const uint32_t item = blockIdx.x * 256u + threadIdx.x;
+    if (item >= p.items) return;
+    const uint32_t t = quotient(item, p.per_token), in_t = item - t * p.per_token.d;
+    const uint32_t group = quotient(in_t, p.per_head), piece = in_t - group * p.per_head.d;
+    const int h0 = (int)group * kRopeHeads;
+    const uint16_t *x = p.x + (int64_t)t * p.xs_t + (int64_t)h0 * p.xs_h + 8 * piece;
+    uint16_t *y = p.y + (int64_t)t * p.ys_t + (int64_t)h0 * p.ys_h + 8 * piece;
+    const int32_t position = p.positions[t];
+    uint4 a[kRopeHeads];
 #pragma unroll
-    for (int n = 0; n < kRopeItems; ++n) {
-        it[n].row = -1;
-        if (base + 256u * n < p.items) it[n] = rope_item(p, base + 256u * n);
-        if (it[n].row >= 0) a[n] = *reinterpret_cast<const uint4 *>(it[n].x + 8 * it[n].piece);
+    for (int h = 0; h < kRopeHeads; ++h)
+        a[h] = h0 + h < p.heads ? *reinterpret_cast<const uint4 *>(x + (int64_t)h * p.xs_h) : make_uint4(0u, 0u, 0u, 0u);
+    const int64_t row = rope_row(position, p.table_rows, p.status);
+    if (row < 0) return;
+    const uint32_t pair = 4 * piece;
+    float2 f[4];
+    if (pair < (uint32_t)p.pairs) {
+        const float2 *cs = p.table + row * p.pairs + pair;
+        if (kWhole) {
+            const float4 f0 = __ldg(reinterpret_cast<const float4 *>(cs)), f1 = __ldg(reinterpret_cast<const float4 *>(cs) + 1);
+            f[0] = make_float2(f0.x, f0.y), f[1] = make_float2(f0.z, f0.w);
+            f[2] = make_float2(f1.x, f1.y), f[3] = make_float2(f1.z, f1.w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = pair + i < (uint32_t)p.pairs ? __ldg(cs + i) : make_float2(0.0f, 0.0f);
+        }
     }
 #pragma unroll
-    for (int n = 0; n < kRopeItems; ++n) {
-        if (it[n].row < 0) continue;
-        uint4 y = a[n];
-        const uint32_t pair = 4 * it[n].piece;
+    for (int h = 0; h < kRopeHeads; ++h) {
+        if (h0 + h >= p.heads) continue;
+        uint32_t w[4] = {a[h].x, a[h].y, a[h].z, a[h].w};
         if (pair < (uint32_t)p.pairs) {
-            const float2 *cs = p.table + it[n].row * p.pairs + pair;
-            float2 f[4];
-            if (kWhole) {
-                const float4 f0 = __ldg(reinterpret_cast<const float4 *>(cs)), f1 = __ldg(reinterpret_cast<const float4 *>(cs) + 1);
-                f[0] = make_float2(f0.x, f0.y), f[1] = make_float2(f0.z, f0.w);
-                f[2] = make_float2(f1.x, f1.y), f[3] = make_float2(f1.z, f1.w);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = pair + i < (uint32_t)p.pairs ? __ldg(cs + i) : make_float2(0.0f, 0.0f);
-            }
-            uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 float lo, hi;
                 rotate(bf16_lo(w[i]), bf16_hi(w[i]), f[i].x, p.sign * f[i].y, lo, hi);
                 if (kWhole || pair + i < (uint32_t)p.pairs) w[i] = bf16x2_from_f32(lo, hi);
             }
-            y = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(it[n].y + 8 * it[n].piece) = y;
+        *reinterpret_cast<uint4 *>(y + (int64_t)h * p.ys_h) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 }
 __global__ void __launch_bounds__(256) k_rope_interleaved(RopeParams p) { rope_interleaved<true>(p); }
