@@ -912,11 +912,11 @@ nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_hea
     if (head_dim % 16 != 0 || K->cols != (int64_t)heads * head_dim) return NVFP4_ERR_SHAPE;
     st = check_workspace(workspace, workspace_bytes, kStatusBytes);
     if (st != NVFP4_OK) return st;
+    if (tokens == 0) return NVFP4_OK;
     if (d_table != nullptr) {
         st = check_rope(d_positions, d_table, table_rows, rotary_dim, interleaved, head_dim);
         if (st != NVFP4_OK) return st;
     }
-    if (tokens == 0) return NVFP4_OK;
     if (k == nullptr || v == nullptr || d_slots == nullptr) return NVFP4_ERR_INVALID_ARG;
     if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(d_slots) & 3u) != 0 ||
         (k_token_stride | k_head_stride | v_token_stride | v_head_stride) % 8 != 0)

@@ -192,6 +192,7 @@ def test_empty_calls_and_binding_refusals():
     none = torch.zeros(0, dtype=torch.int32, device=DEV)
     x = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device=DEV)
     nb.nvfp4_kv_write(x, x, none, kc, vc)
+    nb.nvfp4_kv_write(x, x, none, kc, vc, positions=none, table=torch.zeros(4, 32, 2, device=DEV))
     assert nb.nvfp4_kv_read(kc, vc, none)[0].shape == (0, 128)
     x, slots = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV), torch.zeros(3, dtype=torch.int32, device=DEV)
     with pytest.raises(ValueError, match="slots"):

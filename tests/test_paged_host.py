@@ -136,7 +136,7 @@ def test_write_refusals(lib):
                                   tab, rows, r, inter, ws, wsn, None)
 
     assert call() in DEVICE and call(tab=0, pos=0, r=0) in DEVICE
-    assert call(n=0) == OK
+    assert call(n=0) == OK and call(n=0, k=0, v=0, slots=0, pos=0) == OK
     assert call(n=-1) == ARG and call(h=0) == ARG and call(kt=-8) == ARG
     assert call(d=120) == SHAPE and call(h=3) == SHAPE
     assert call(K=_pools(layout=0)) == SHAPE and call(V=_pools(rows=32)) == SHAPE
