@@ -29,8 +29,8 @@
 // scales are whole 16-byte groups, a stage's parts are boxes of a 3-D tiled
 // TMA load (bytes of a head x 16 rows x heads), swizzled by it; else each
 // token's row is looked up and copied in 16-byte pieces by cp.async to the
-// same places (pages of 20 tokens: 64 x 8192 in 171 us, bound by the copying
-// warps' instructions).  Computing warps that refilled the ring themselves took 150 us
+// same places (64 x 8192 in pages of 20 tokens: 135 us; with addresses worked
+// out piece by piece 171, the copying warps' instructions being the bound).  Computing warps that refilled the ring themselves took 150 us
 // against 130 at 64 x 8192 (registers).
 //
 // Schedule.  The sequences' tiles (16 tokens times the warps of a unit; an
@@ -82,12 +82,12 @@ constexpr float kSlack = 14.0f;      // a score may pass m' by this before m' mo
 
 constexpr int kWarps = 8;            // warps that compute
 // Warps that bring the tiles in, stages in turn.  Copies by cp.async take four
-// where the registers of two further warps are free (4 x 3 .. 97886 tokens, 5
-// heads x 64: 50.1 -> 42.8 us; 112 x 270 .. 574, 5 x 256: 43.6 -> 41.1; with
-// heads of 128 values 80 registers spill: 64 x 8192 in pages of 20 171 -> 179).
+// with heads of 64 values (4 x 3 .. 97886 tokens, 5 heads: 43.5 -> 39.6 us);
+// with 128 the 80 registers that are left spill (64 x 8192 in pages of 20: 5 %
+// slower with three), with 256 it is 3 % either way.
 template <int kD, bool kTma>
 struct Producers {
-    static constexpr int kCount = kTma || kD == 128 ? 2 : 4;
+    static constexpr int kCount = !kTma && kD == 64 ? 4 : 2;
 };
 constexpr long long kDrainCycles = 2000000000ll;   // bound of the wait for copies under way (about a second)
 constexpr int kTile = 16;            // tokens of a warp's tile
@@ -303,6 +303,59 @@ struct Cursor {
         }
     }
 };
+
+// A stage's rows by cp.async: 16-byte pieces of 2^kHeadsShift heads' codes, and
+// kScales bytes of each head's scales, to where the boxes of TMA would lie.  A
+// lane keeps its place in the rows; token t0 + i (t0 a lane's, i a multiple of
+// the lanes' tokens) adds constants, as the swizzle is an xor of token bits.
+template <int kD, int kPartsShift, int kHeadsShift>
+__device__ __forceinline__ void copy_rows(const PagedAttnParams &p, const int *rows, uint32_t to, int head_first) {
+    using S = Shape<kD>;
+    constexpr int kHeads = 1 << kHeadsShift, kTokens = kTile << kPartsShift, kCodesTile = kTile * S::kCodes;
+    constexpr uint32_t kV = kHeads * kTokens * S::kCodes;               // from K's codes to V's
+    constexpr int kGroups = kHeads * S::kScales > 16 ? kHeads * S::kScales / 16 : 1;
+    constexpr uint32_t kVScales = kGroups * kTokens * 16;
+    const int lane = threadIdx.x & 31;
+    {
+        constexpr int kLanes = kHeads * S::kChunks, kStep = 32 / kLanes;    // lanes of a token, tokens of a step
+        constexpr int kUnroll = kTokens / kStep < 8 ? kTokens / kStep : 8;  // 8 tokens or more: whole periods of the swizzle
+        static_assert(kLanes <= 32 && kTokens % (kUnroll * kStep) == 0 && kUnroll * kStep >= 8, "whole rounds");
+        const int x = lane % kLanes, t0 = lane / kLanes;
+        const uint8_t *kc = p.kc + (int64_t)head_first * S::kCodes + 16 * x;
+        const uint8_t *vc = p.vc + (int64_t)head_first * S::kCodes + 16 * x;
+        const uint32_t dst = to + (x / S::kChunks) * kCodesTile + t0 * S::kCodes + 16 * swizzled<kD>(x % S::kChunks, t0);
+#pragma unroll 1
+        for (int t = 0; t < kTokens; t += kUnroll * kStep) {
+            const uint32_t at = (uint32_t)(t / kTile) * (kHeads * kCodesTile) + (t % kTile) * S::kCodes;
+            int r[kUnroll];
+#pragma unroll
+            for (int n = 0; n < kUnroll; ++n) r[n] = rows[t + t0 + n * kStep];
+#pragma unroll
+            for (int n = 0; n < kUnroll; ++n) {
+                const int i = n * kStep;
+                const uint32_t d = (dst ^ (16 * swizzled<kD>(0, i))) + at + (i / kTile) * (kHeads * kCodesTile) + (i % kTile) * S::kCodes;
+                if (r[n] >= 0) {
+                    copy_async<16>(d, kc + (int64_t)r[n] * p.row_codes);
+                    copy_async<16>(d + kV, vc + (int64_t)r[n] * p.row_codes);
+                }
+            }
+        }
+    }
+    constexpr int kStep = 32 / kHeads;
+    const int h = lane % kHeads, t0 = lane / kHeads, byte = (head_first + h) * S::kScales;     // of a row's scales
+    const uint32_t dst = to + 2 * kV + ((byte - ((head_first * S::kScales) & ~15)) >> 4) * (16 * kTile) + (byte & 15) +
+                         (t0 / kTile) * (kGroups * 16 * kTile) + (t0 % kTile) * 16;
+    const uint8_t *ks = p.ks + byte, *vs = p.vs + byte;
+#pragma unroll
+    for (int i = 0; i < kTokens; i += kStep) {
+        const int r = rows[t0 + i];
+        const uint32_t d = dst + (i / kTile) * (kGroups * 16 * kTile) + (i % kTile) * 16;
+        if (r >= 0) {
+            copy_async<S::kScales>(d, ks + (int64_t)r * p.row_scales);
+            copy_async<S::kScales>(d + kVScales, vs + (int64_t)r * p.row_scales);
+        }
+    }
+}
 
 }  // namespace
 
@@ -543,13 +596,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             // head's scales.
             const int tokens_stage = kTile << kPartsShift;
             int *rows = rows_sh[warp - kWarps];
-            const int piece_shift = plan.heads_shift + (kD == 64 ? 1 : kD == 128 ? 2 : 3);
-            // a lane's place in the rows' pieces and scales, the same in every step (both are at most 32 a token)
-            const int x = lane & ((1 << piece_shift) - 1), h = lane & (heads_cta - 1);
-            const uint8_t *kc = p.kc + (int64_t)head_first * S::kCodes + 16 * x, *vc = p.vc + (int64_t)head_first * S::kCodes + 16 * x;
-            const int byte = (head_first + h) * S::kScales;             // of a row's scales
-            const uint32_t codes_at = (uint32_t)(x / S::kChunks) * (kTile * S::kCodes);
-            const uint32_t scales_at = k_scales + (uint32_t)((byte - ((head_first * S::kScales) & ~15)) >> 4) * (16 * kTile) + (byte & 15);
             int pages[4], offsets[4];                                   // tokens lane, lane + 32, ...
             auto lookup = [&]() {
 #pragma unroll
@@ -595,25 +641,11 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 lookup();
                 __syncwarp();
                 const uint32_t to = ring + stage * plan.stage_bytes;
-#pragma unroll 4
-                for (int t = lane >> piece_shift; t < tokens_stage; t += 32 >> piece_shift) {
-                    const int r = rows[t];
-                    const uint32_t dst = to + codes_at + ((t >> 4) << plan.heads_shift) * (kTile * S::kCodes) +
-                                         (t & 15) * S::kCodes + 16 * swizzled<kD>(x % S::kChunks, t & 15);
-                    if (r >= 0) {
-                        copy_async<16>(dst, kc + (int64_t)r * p.row_codes);
-                        copy_async<16>(dst + v_codes, vc + (int64_t)r * p.row_codes);
-                    }
-                }
-#pragma unroll 4
-                for (int t = lane >> plan.heads_shift; t < tokens_stage; t += 32 >> plan.heads_shift) {
-                    const int r = rows[t];
-                    const uint32_t dst = to + scales_at + (t >> 4) * scale_groups * (16 * kTile) + (t & 15) * 16;
-                    if (r >= 0) {
-                        copy_async<S::kScales>(dst, p.ks + (int64_t)r * p.row_scales + byte);
-                        copy_async<S::kScales>(dst + (v_scales - k_scales), p.vs + (int64_t)r * p.row_scales + byte);
-                    }
-                }
+                if (plan.heads_shift == 0) copy_rows<kD, kPartsShift, 0>(p, rows, to, head_first);
+                if constexpr (kPartsShift < 3)
+                    if (plan.heads_shift == 1) copy_rows<kD, kPartsShift, 1>(p, rows, to, head_first);
+                if constexpr (kPartsShift < 2)
+                    if (plan.heads_shift == 2) copy_rows<kD, kPartsShift, 2>(p, rows, to, head_first);
                 copies_arrive(&full[stage]);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[stage]);               // the masks
@@ -1069,7 +1101,7 @@ cudaError_t launch_dependent(const void *kernel, dim3 grid, int threads, size_t 
 template <int kD, bool kTma, int kPartsShift>
 cudaError_t launch_main(const PagedAttnParams &p, const PagedMaps &maps, cudaStream_t s) {
     constexpr int kProducers = Producers<kD, kTma>::kCount;
-    // a producer that is not a stage behind itself could mistake a barrier's phase
+    // with fewer stages a producer could take a barrier's phase for the one after
     if (p.plan.stages < kProducers) return cudaErrorInvalidConfiguration;
     static std::atomic<uint64_t> ready{0};               // devices (below 64) with the shared memory allowed
     const void *kernel = (const void *)k_paged_attention<kD, kTma, kPartsShift>;
