@@ -91,6 +91,7 @@ struct Producers {
 };
 constexpr long long kDrainCycles = 2000000000ll;   // bound of the wait for copies under way (about a second)
 constexpr int kTile = 16;            // tokens of a warp's tile
+constexpr int kProducerBarrier = 8;  // named barrier of the producers (1 .. 4: the units')
 
 template <int kD>
 struct Shape {
@@ -367,6 +368,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t full[kPagedMaxStages], empty[kPagedMaxStages];
     __shared__ int masks[kPagedMaxStages][kWarps];
+    __shared__ int armed[kPagedMaxStages];               // 1 + parity of the phase of `full` that was armed last, 0: none (TMA)
     __shared__ int rows_sh[kProducers][kWarps * kTile];  // pool rows of a stage's tokens (copies without TMA)
     __shared__ float4 ml[kWarps][4];                     // (m, l) of heads 2c and 2c + 1
     __shared__ uint32_t warp_sums[kWarps + kProducers];
@@ -377,6 +379,7 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
     if (tid < p.plan.stages) {
         mbar_init(&full[tid], kTma ? 1 : 33);
         mbar_init(&empty[tid], kWarps);
+        armed[tid] = 0;
     }
     fence_barrier_init();
     // what is read from here on may be the result of the kernels before
@@ -534,10 +537,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 return f;
             };
             const uint32_t bytes = 2u * (part_codes + part_scales);
-            // Stages that this warp has armed, the parity of their `full`, and
-            // those that no later tile uses.
-            uint32_t armed = 0, parity = 0, last = 0;
-            int tiles_left = count;                                     // from the first of the batch
             Batch f = lookup();
             while (f.n > 0) {
                 const Batch next = lookup();
@@ -552,7 +551,6 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         advance();
                         continue;
                     }
-                    const int tile = count - tiles_left + i;
                     const int from = (i << kPartsShift) + my_part;
                     const int my_row = __shfl_sync(0xFFFFFFFFu, row, from);
                     const int tokens = __shfl_sync(0xFFFFFFFFu, f.tokens, from);
@@ -561,10 +559,10 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     if (failed) break;
                     if (lane < tw) masks[stage][lane] = (1 << tokens) - 1;
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_expect_tx(&full[stage], __popc(there) * bytes);
-                    armed |= 1u << stage;
-                    parity = (parity & ~(1u << stage)) | ((phase ^ 1u) << stage);
-                    if (tile + plan.stages >= count) last |= 1u << stage;
+                    if (lane == 0) {
+                        armed[stage] = 1 + (int)(phase ^ 1u);
+                        mbar_arrive_expect_tx(&full[stage], __popc(there) * bytes);
+                    }
                     uint32_t to = ring + stage * plan.stage_bytes, scales = to + k_scales;
 #pragma unroll 1
                     for (int n = 0; n < tw; ++n, to += part_codes, scales += part_scales) {
@@ -580,15 +578,15 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                     advance();
                 }
                 if (failed) break;
-                tiles_left -= f.n;
                 f = next;
             }
             // No copy may be under way when the CTA ends, whoever has given up
-            // waiting for it.
-            const uint32_t await = failed ? armed : last;
+            // waiting for it: once neither warp arms a stage any more, the
+            // phase that was last armed of each is awaited.
+            unit_barrier(kProducerBarrier, 32 * kProducers);
 #pragma unroll 1
             for (int n = 0; n < plan.stages; ++n)
-                if ((await >> n) & 1u) bounded_wait(&full[n], (parity >> n) & 1u, kDrainCycles);
+                if (armed[n] != 0) bounded_wait(&full[n], (uint32_t)armed[n] - 1u, kDrainCycles);
         } else {
             // Pages that end inside of a tile, or rows that TMA cannot step
             // by: the rows of a stage's tokens are looked up one stage ahead,
@@ -757,8 +755,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
         left -= n_tiles;
 #pragma unroll 1
         for (int tile = n_tiles; tile > 0; --tile) {
-            // A wait that gives up leaves the CTA in step: its tiles then
-            // count as empty, every barrier is still met.
+            // A wait that gives up leaves the unit in step: its tiles then
+            // count as empty, every barrier of the unit is still met.
             if (!failed && !ready) {
                 failed = !__all_sync(0xFFFFFFFFu, bounded_wait(&full[stage], phase, p.timeout));
                 if (failed) set_status(p.status, ST_TIMEOUT);
@@ -886,8 +884,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
                 for (int k = 0; k < 4; ++k) mma_f16(oacc[4 * n + k], even[0][k], odd[0][k], even[1][k], odd[1][k], p0, p1);
             }
+            // A warp that has given up hands no stage back, so that none is
+            // armed again before all warps have seen its copies land; the
+            // producers' own waits then run out.  (Leaving the loop instead
+            // was 2 % slower at 64 x 8192.)
             warp_sync();
-            if (lane == 0) mbar_arrive(&empty[stage]);
+            if (lane == 0 && !failed) mbar_arrive(&empty[stage]);
             at += plan.stage_bytes;
             if (++stage == plan.stages) {
                 stage = 0;
