@@ -130,6 +130,21 @@ def _query(n, heads, dim, seed):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["long", "ragged"])
+@pytest.mark.parametrize("dim,heads,page", FORMS)
+def test_stages_are_used_again(dim, heads, page, kind):
+    lens = _lengths(dim, heads, kind)
+    pool = Pool(lens, dim, heads, page, dim + heads + page)
+    q = _query(len(lens), heads, dim, 1)
+    ws = nb.Workspace(DEV, 256)
+    o, lse = pool.attend(q, workspace=ws)
+    assert nb.nvfp4_check_status(ws) == 0
+    pool.check(q, o, lse, dim ** -0.5)
+    again, l2 = pool.attend(q, workspace=ws)
+    assert torch.equal(R.bits(o), R.bits(again)) and torch.equal(lse, l2)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("limit", [1, 1000, 20000])
 @pytest.mark.parametrize("dim,heads,page", [(128, 40, 16), (256, 21, 16), (64, 40, 20), (128, 37, 16)])   # TMA, TMA, cp.async, cp.async
 def test_a_wait_that_gives_up_with_stages_in_use(dim, heads, page, limit):
