@@ -718,7 +718,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
 #pragma unroll
             for (int n = 0; n < kD / 32; ++n) {
                 const int d = kD == 256 ? 32 * c + 8 * (n & 3) + 128 * (n >> 2) : (kD / 4) * c + 8 * n;
-                w[n] = g < heads ? __ldg(reinterpret_cast<const uint4 *>(q + d)) : make_uint4(0u, 0u, 0u, 0u);
+                // a plain load: o may be q, which the kernel then writes
+                w[n] = g < heads ? *reinterpret_cast<const uint4 *>(q + d) : make_uint4(0u, 0u, 0u, 0u);
                 amax = max_u16x2(amax, max_u16x2(max_u16x2(w[n].x & 0x7FFF7FFFu, w[n].y & 0x7FFF7FFFu),
                                                  max_u16x2(w[n].z & 0x7FFF7FFFu, w[n].w & 0x7FFF7FFFu)));
             }

@@ -168,3 +168,19 @@ def test_a_wait_that_gives_up_with_stages_in_use(dim, heads, page, limit):
     o, lse = pool.attend(q, workspace=ws)
     assert nb.nvfp4_check_status(ws) == 0
     pool.check(q, o, lse, dim ** -0.5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,heads,page", [(64, 40, 16), (128, 38, 16), (128, 37, 16), (256, 22, 5)])
+def test_output_in_place_of_the_queries_of_many_sequences(dim, heads, page):
+    """CTAs that take several sequences fetch a query while they write the
+    result before it; sequences that are cut leave theirs to the join."""
+    lens = _lengths(dim, heads, "ragged")
+    pool = Pool(lens, dim, heads, page, 11)
+    rows = torch.full((len(lens), heads * GROUP * dim + 24), 7.0, dtype=torch.bfloat16, device=DEV)
+    q = rows[:, 8:-16].view(len(lens), heads * GROUP, dim)                 # rows that share cache lines with their neighbours
+    q.copy_(_query(len(lens), heads, dim, 3))
+    o, lse = pool.attend(q)
+    got, got_lse = pool.attend(q, out=q)
+    assert got is q and torch.equal(R.bits(q), R.bits(o)) and torch.equal(got_lse, lse)
+    assert (rows[:, :8] == 7).all() and (rows[:, -16:] == 7).all()
