@@ -445,7 +445,10 @@ def _switched(device, stream):
             yield
         else:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
+                # 0 and 1 (cudaStreamLegacy) are the default stream; torch
+                # takes a null handle for "any stream of the pool"
+                stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
+                          else torch.cuda.ExternalStream(int(stream), device=device))
             with torch.cuda.stream(stream):
                 yield
 
