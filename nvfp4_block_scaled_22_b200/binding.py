@@ -449,6 +449,8 @@ def _switched(device, stream):
                 # takes a null handle for "any stream of the pool"
                 stream = (torch.cuda.default_stream(device) if int(stream) in (0, 1)
                           else torch.cuda.ExternalStream(int(stream), device=device))
+            elif stream.device_index != _current_device():
+                raise ValueError(f"stream is not on cuda:{_current_device()}, the device of the first argument")
             with torch.cuda.stream(stream):
                 yield
 

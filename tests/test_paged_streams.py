@@ -48,6 +48,16 @@ def test_the_stream_that_a_handle_names(made_current, stream, name):
     assert made_current == [name]
 
 
+def test_a_stream_of_another_device_is_refused(made_current):
+    """Made current, it would leave the call on the tensors' own device's current stream."""
+    with pytest.raises(ValueError, match="stream is not on cuda:0"):
+        with nb._switched(torch.device("cuda", 0), FakeStream(index=1)):
+            raise AssertionError("the call would have run")
+    with nb._switched(torch.device("cuda"), FakeStream(index=0)):       # the current device
+        pass
+    assert made_current == ["given"]
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("handle", [0, 1])
 def test_handle_of_the_default_stream_keeps_the_order_of_its_work(handle):
