@@ -51,9 +51,10 @@
 //   p = 2^(S c - m'), c = scale log2(e) / g_K and the query's power of two
 //     undone.  m' is 6 below a running reference that is moved (and what was
 //     summed rescaled) only when a score passes it by 8: p stays within
-//     2^14, and the largest p of a head is at least 2^6, so that rounding p
-//     to FP16 for the product with V costs 2^-11 of each weight, or 2^-31 of
-//     the largest for tiny ones.  The sum l takes the unrounded p in FP32.
+//     2^14, and the largest p of a head is at least 2^6 (scores past 2^23: 2^0),
+//     so that rounding p to FP16 for the product with V costs 2^-11 of each
+//     weight, or 2^-31 of the largest for tiny ones.  The sum l takes the
+//     unrounded p in FP32.
 //   O^T[dim x 8 heads] += V^T P^T, the same MMA: P goes from accumulator to
 //     operand layout by movmatrix; the codes of two tokens are interleaved
 //     by nibbles so that one conversion gives the two tokens of one dim.
@@ -845,8 +846,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                         oacc[j][n] *= alpha;
                         oacc[j][n + 2] *= alpha;
                     }
-                    if (r0) e[n] = __fmaf_rn(s[n], ck[n], -mn);
-                    if (r1) e[n + 2] = __fmaf_rn(s[n + 2], ck[n], -mn);
+                    // From the rounded x, as mn is: the exact product is off from
+                    // x by 16 at 2^28, which would take the largest weight out of
+                    // FP16's range on either side.  A score past FP32's range
+                    // gives inf - inf, NaN in its head.
+                    if (r0) e[n] = __fsub_rn(x0, mn);
+                    if (r1) e[n + 2] = __fsub_rn(x1, mn);
                 }
             }
 #pragma unroll
