@@ -223,10 +223,18 @@ _default_ws: dict[int, Workspace] = {}
 
 
 def default_workspace(device=None) -> Workspace:
+    """The device's workspace of calls that are given none, made by the first
+    of them.  Make it before a CUDA graph is captured (by a call outside, or by
+    this one): made inside, each replay fills it anew, and with that clears
+    what the replays before recorded."""
     dev = torch.device(device or "cuda")
     idx = dev.index if dev.index is not None else torch.cuda.current_device()
     if idx not in _default_ws:
-        _default_ws[idx] = Workspace(torch.device("cuda", idx))
+        ws = Workspace(torch.device("cuda", idx))
+        # filled before a call on another stream uses it
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(idx).synchronize()
+        _default_ws[idx] = ws
     return _default_ws[idx]
 
 

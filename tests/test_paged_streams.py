@@ -92,3 +92,41 @@ def test_handle_of_the_default_stream_keeps_the_order_of_its_work(handle):
     torch.cuda.synchronize()
     assert torch.equal(y, want) and torch.equal(got[0], rows[0]) and torch.equal(got[1], rows[1]) and torch.equal(z, o)
     assert nb.nvfp4_check_status() == 0
+
+
+@pytest.mark.parametrize("capturing", [False, True])
+def test_the_default_workspace_is_filled_before_it_is_handed_out(monkeypatch, capturing):
+    """Its zeros are written on the stream of the first call; a later call on
+    another stream is not ordered behind them.  Inside of a capture there is
+    nothing to wait for."""
+    done = []
+
+    class Stream:
+        def synchronize(self):
+            assert done == ["filled on cuda:0"] and not nb._default_ws
+            done.append("waited")
+
+    monkeypatch.setattr(nb, "_default_ws", {})
+    monkeypatch.setattr(nb, "Workspace", lambda device: done.append(f"filled on {device}") or object())
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    ws = nb.default_workspace(torch.device("cuda", 0))
+    assert done == ["filled on cuda:0"] + ["waited"] * (not capturing)
+    assert nb.default_workspace(torch.device("cuda", 0)) is ws and len(done) == 2 - capturing
+
+
+@pytest.mark.gpu
+def test_an_error_recorded_behind_a_first_call_on_a_busy_stream_is_kept(monkeypatch):
+    monkeypatch.setattr(nb, "_default_ws", {})
+    table = nb.nvfp4_rope_table(nb.nvfp4_rope_inv_freq(64), 16, device=DEV)
+    x = torch.ones(4, 2, 64, dtype=torch.bfloat16, device=DEV)
+    good, bad = (torch.full((4,), p, dtype=torch.int32, device=DEV) for p in (3, 99))
+    busy = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(busy):
+        torch.cuda._sleep(20_000_000)                                    # 10 ms
+        nb.nvfp4_rope(x, good, table)                                    # makes the default workspace here
+    nb.nvfp4_rope(x, bad, table)
+    torch.cuda.synchronize()
+    assert nb.nvfp4_check_status() == 1
+    assert nb.nvfp4_check_status() == 0
