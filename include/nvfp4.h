@@ -415,8 +415,9 @@ NVFP4_API nvfp4_status nvfp4_rope(const void *x, int64_t x_token_stride, int64_t
  * k, v: BF16 [tokens][heads][head_dim], strides in elements, multiples of 8;
  *   16-byte aligned.  head_dim % 16 == 0, heads * head_dim == K->cols.
  * Two tokens of one call may not name the same slot, nor K and V share their
- * buffers unless equal bytes go there (the row would hold parts of both).  Non-finite values are recorded as NVFP4_ERR_NONFINITE; the
- * 16-value block that holds them is then unspecified. */
+ * buffers unless equal bytes go there (the row would hold parts of both).
+ * Non-finite values are recorded as NVFP4_ERR_NONFINITE; the 16-value block
+ * that holds them is then unspecified. */
 NVFP4_API nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int64_t k_head_stride,
                                       const void *v, int64_t v_token_stride, int64_t v_head_stride,
                                       int64_t tokens, int32_t heads, int32_t head_dim,
@@ -429,8 +430,8 @@ NVFP4_API nvfp4_status nvfp4_kv_write(const void *k, int64_t k_token_stride, int
 /* Read rows back: k[r], v[r] = BF16 of pool row d_slots[r] of K and V, as
  * nvfp4_dequantize restores them; slot -1 (or out of range) gives zeros.
  * k, v: BF16 [rows x cols], pitches ldk, ldv elements (multiples of 8),
- * 16-byte aligned, two arrays.  For the dense attention of a prompt chunk over what is
- * cached already. */
+ * 16-byte aligned, two arrays.  For the dense attention of a prompt chunk over
+ * what is cached already. */
 NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *V,
                                      const int32_t *d_slots, int64_t rows, void *k, int64_t ldk,
                                      void *v, int64_t ldv, void *workspace, size_t workspace_bytes,
@@ -443,14 +444,20 @@ NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *
  * page_size:
  *   s_t = scale * q_h . k_t,  o_h = sum_t exp(s_t) v_t / sum_t exp(s_t),
  *   d_lse[b * heads_q + h] = log sum_t exp(s_t)   (d_lse may be NULL)
- * with k, v the exact restored values.  A sequence of length 0 gives o = 0
- * and lse = -inf.  A length past table_pages * page_size (or below 0) is cut
- * to it (to 0) and recorded as NVFP4_ERR_INVALID_ARG; tokens on a page
- * outside of the pool take no part and are recorded alike.
+ * with k, v the exact restored values, q to 2^-29 of a head's largest, scores
+ * and sums in FP32.  The weights
+ * that multiply v are rounded to FP16 (by 2^-11 of each, or 2^-31 of the
+ * largest of a head for small ones; nvfp4_attention_decode multiplies them
+ * unrounded), o to BF16 once.  A score past FP32's range makes its head NaN.
+ * A sequence of length 0 gives o = 0 and lse = -inf.  A length past
+ * table_pages * page_size (or below 0) is cut to it (to 0) and recorded as
+ * NVFP4_ERR_INVALID_ARG; tokens on a page outside of the pool take no part and
+ * are recorded alike.
  * q, o  : BF16 [sequences][heads_q][head_dim], strides in elements, multiples
  *         of 8; 16-byte aligned.  o == q with equal strides works in place;
  *         they may not overlap in part.  head_dim = K->cols / heads_kv: 64,
  *         128, 256.  heads_q < 2^16.
+ * table_stride: at least table_pages where there are two sequences or more.
  * page_size: any; K->rows a multiple of it and below 2^31.  table_pages *
  *   page_size < 2^31 - 1024, sequences * (table_pages * page_size / 16 + 8) < 2^31.
  * scratch: nvfp4_attention_paged_scratch_bytes(heads_q, heads_kv, head_dim)

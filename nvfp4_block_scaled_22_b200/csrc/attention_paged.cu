@@ -8,10 +8,10 @@
 // registers.  Bound: the read, and close behind it the instructions that
 // restore and multiply -- a 16-token tile of 8 heads x 128 dims takes a warp
 // about 280, two of a lane's a value -- so that the long calls end between
-// the two: 64 sequences of 8192 tokens, 8 KV heads x 128, 64 query heads 116
-// us (5.0 TB/s, 0.77 of a copy); one of 131072 tokens 40.6 us (3.7 TB/s; each
+// the two: 64 sequences of 8192 tokens, 8 KV heads x 128, 64 query heads 120
+// us (5.1 TB/s, 0.77 of a copy); one of 131072 tokens 40.6 us (3.7 TB/s; each
 // further 131072 take 26 us, 5.8 TB/s, the rest is start, ending and join);
-// 96 of 256 to 8192 tokens 60 us (4.2 TB/s).  One of 1000 tokens takes 9.5
+// 96 of 256 to 8192 tokens 60 us (4.2 TB/s).  One of 1000 tokens takes 9.8
 // us, of one token 6: two launches and four dependent reads (length, page,
 // tile, parts).
 //
@@ -29,9 +29,10 @@
 // scales are whole 16-byte groups, a stage's parts are boxes of a 3-D tiled
 // TMA load (bytes of a head x 16 rows x heads), swizzled by it; else each
 // token's row is looked up and copied in 16-byte pieces by cp.async to the
-// same places (64 x 8192 in pages of 20 tokens: 135 us; with addresses worked
-// out piece by piece 171, the copying warps' instructions being the bound).  Computing warps that refilled the ring themselves took 150 us
-// against 130 at 64 x 8192 (registers).
+// same places (64 x 8192 in pages of 20 tokens: 139 us; with addresses worked
+// out piece by piece 27 % more, the copying warps' instructions being the
+// bound).  Computing warps that refilled the ring themselves took 150 us where
+// a producer warp took 130 (registers).
 //
 // Schedule.  The sequences' tiles (16 tokens times the warps of a unit; an
 // empty sequence counts one), each sequence's behind some that stand for the

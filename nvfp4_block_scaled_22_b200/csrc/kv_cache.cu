@@ -15,9 +15,11 @@
 //
 // Both are bound by memory (2.56 bytes a value): 131072 rows of 2 x 1024
 // values are read back in 108 us (6.4 TB/s), 16384 tokens of 2 x 8 x 128
-// written in 17.7 us (4.9 TB/s, launch included), with rotated keys in 23.9
-// us -- a key block then costs 12 instructions a value, on loads that wait
-// for the position and then for the table row.  Tried for the write: a half
+// written in 17.8 us (4.8 TB/s, launch included), with rotated keys in 24.2
+// us (interleaved 27.3): the table rows are loaded behind slot and position,
+// outside of the one item that a thread fetches ahead, and 19 warps an SM do
+// not hide that (a warp waits for loads 3.7 cycles an instruction issued; 57 %
+// of the issue slots are used).  Tried for the write: a half
 // block a thread (30 us: the scale's arithmetic twice), two heads a thread
 // that share table entries (27.6 us: registers), tables for the divisions
 // (26.5 us).

@@ -12,8 +12,10 @@
 // reduced to a turn, so an FP32 angle is off by 0.06 at position 2^20.
 //
 // Bound by memory: 4 bytes a value against 3 FP32 operations (8192 x 72 x 128
-// in 47.5 us, 6.4 TB/s; interleaved 46.4; 4099 x 40 x 128 interleaved, half
-// rotated, in 14.9 us).
+// in 47.6 us, 6.4 TB/s; interleaved 46.4; 4099 x 40 x 128 interleaved, half
+// rotated, in 14.5 us).  The table, made once, is bound by its arithmetic: 125
+// instructions an entry of FP64 sine and cosine and a division (131072
+// positions x 64 pairs in 36.3 us, 80 % of the issue slots; its bytes: 10.2 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
