@@ -728,9 +728,10 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             uint32_t e = max(amax & 0xFFFFu, amax >> 16) >> 7;          // exponent field of the largest value
             e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
             e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
-            // times 2^(14 - (e - 127)), within FP32's exponents; a query of
-            // zeros, infinities or NaN stays as it is
-            const int up = e == 0u || e == 255u ? 0 : min(141 - (int)e, 126);
+            // times 2^(14 - (e - 127)), within FP32's exponents (so that a
+            // query of subnormal values is held, exactly); one with infinities
+            // or NaN stays as it is
+            const int up = e == 255u ? 0 : min(141 - (int)e, 126);
             const float mult = __uint_as_float((uint32_t)(127 + up) << 23);
             const float undo = __uint_as_float((uint32_t)(127 - up) << 23);
 #pragma unroll

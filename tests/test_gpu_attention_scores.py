@@ -53,3 +53,21 @@ def test_scores_past_fp32_are_nan_in_their_head():
     bad = torch.zeros(2, 8, dtype=torch.bool)
     bad[0, 3] = True
     assert torch.isnan(o.float()).all(-1).cpu().equal(bad) and torch.isnan(lse).cpu().equal(bad)
+
+
+@pytest.mark.parametrize("dim,heads", [(64, 4), (128, 2), (256, 1)])
+@pytest.mark.parametrize("exponent", [-126, -128, -131])
+def test_queries_of_subnormal_values(dim, heads, exponent):
+    """What BF16 still holds of such a query, with a scale that brings its
+    scores back to the order of one."""
+    cache = Cache([300, 7], heads, dim, 16, 53)
+    q = _query(2, heads * 8, dim, 54, 2.0 ** exponent)
+    scale = 2.0 ** -exponent * dim ** -0.5 / 4
+    o, lse = cache.attend(q.to(DEV), scale=scale)
+    for b, n in enumerate(cache.lens):
+        k, v = cache.host[b]
+        want, wl, ao, sa = R.attention(R.f64(q[b]).reshape(heads, -1, dim), k, v, float(np.float32(scale)))
+        ob, lb = R.attention_bounds(want, wl, ao, sa, n, dim, np.abs(v).max())
+        assert np.ptp(wl) > 10 * lb.max()                      # scores that are all 0 would show
+        assert np.all(np.abs(R.f64(o[b]).reshape(want.shape) - want) <= ob)
+        assert np.all(np.abs(R.f64(lse[b]).reshape(wl.shape) - wl) <= lb)
