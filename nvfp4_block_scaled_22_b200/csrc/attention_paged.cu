@@ -198,6 +198,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return d;
 }
 
+// 1 / (l g), or 0 for no token, as a product of two factors: g is up to 2^118,
+// so that neither l g nor its reciprocal need be a normal number.  `post` is a
+// power of two (1 up to g = 2^60), the bits are those of one factor where it
+// would do.
+__device__ __forceinline__ float post_of(float g) { return g > 0x1p60f ? 0x1p-60f : 1.0f; }
+__device__ __forceinline__ float share_of(float l, float g, float post) {
+    return l == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(l, g * post));
+}
+
 // log of a sum l of 2^(x - m), natural; lg2.approx is off by at most 2^-22
 // (l is 0 or at least 1)
 __device__ __forceinline__ float lse_of(float m, float l) {
@@ -940,11 +949,12 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
             L[1] += v.w * exp2_fast(v.z - M[1]) + u.w * exp2_fast(u.z - M[1]);
         }
         const bool whole = ends && starts_here;
-        float f[2] = {1.0f, 1.0f};
+        float f[2] = {1.0f, 1.0f}, post = 1.0f;
         if (whole) {
             const float gv = __ldg(p.gv);
+            post = post_of(gv);
 #pragma unroll
-            for (int n = 0; n < 2; ++n) f[n] = L[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(L[n], gv));
+            for (int n = 0; n < 2; ++n) f[n] = share_of(L[n], gv, post);
         }
         const int h = head0 + 2 * c;
         const bool h0 = 2 * c < heads, h1 = 2 * c + 1 < heads;
@@ -966,8 +976,8 @@ k_paged_attention(const __grid_constant__ PagedAttnParams p, const __grid_consta
                 r[3] += v.w * f1 + u.w * g1;
             }
             if (whole) {
-                if (h0) *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0], r[2] * f[0]);
-                if (h1) *reinterpret_cast<uint32_t *>(o + p.os_h + 2 * j) = bf16x2_from_f32(r[1] * f[1], r[3] * f[1]);
+                if (h0) *reinterpret_cast<uint32_t *>(o + 2 * j) = bf16x2_from_f32(r[0] * f[0] * post, r[2] * f[0] * post);
+                if (h1) *reinterpret_cast<uint32_t *>(o + p.os_h + 2 * j) = bf16x2_from_f32(r[1] * f[1] * post, r[3] * f[1] * post);
             } else {
                 part_o[32 * j] = make_float4(r[0], r[1], r[2], r[3]);
             }
@@ -1078,13 +1088,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_paged_combine(const __grid_
         if (mine == 0 && item < items) {
             const int hk = unit / p.plan.units_head, sub = unit - hk * p.plan.units_head;
             const int h = hk * p.group + sub * 8 + 2 * c, heads = min(8, p.group - sub * 8) - 2 * c;
-            const float gv = __ldg(p.gv);
+            const float gv = __ldg(p.gv), post = post_of(gv);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 if (n < heads) {
-                    const float f = l[n] == 0.0f ? 0.0f : __frcp_rn(__fmul_rn(l[n], gv));
+                    const float f = share_of(l[n], gv, post);
                     *reinterpret_cast<uint32_t *>(p.o + (int64_t)b * p.os_b + (int64_t)(h + n) * p.os_h + (dim / 8) * g + 2 * j) =
-                        bf16x2_from_f32(a[n] * f, a[n + 2] * f);
+                        bf16x2_from_f32(a[n] * f * post, a[n + 2] * f * post);
                     if (j == 0 && g == 0 && p.lse != nullptr) p.lse[(int64_t)b * p.heads_q + h + n] = lse_of(m[n], l[n]);
                 }
             }

@@ -71,3 +71,22 @@ def test_queries_of_subnormal_values(dim, heads, exponent):
         assert np.ptp(wl) > 10 * lb.max()                      # scores that are all 0 would show
         assert np.all(np.abs(R.f64(o[b]).reshape(want.shape) - want) <= ob)
         assert np.all(np.abs(R.f64(lse[b]).reshape(wl.shape) - wl) <= lb)
+
+
+@pytest.mark.parametrize("dim,heads,page", [(64, 4, 16), (128, 2, 20), (256, 1, 16)])
+@pytest.mark.parametrize("exponent", [-100, 60, 61, 100, 118])
+def test_value_scales_of_the_whole_range(dim, heads, page, exponent):
+    """A tensor scale of V is up to 2^118 (nvfp4_quantize) and down to 2^-116
+    (of BF16's largest values): a power of two in it is one in the output,
+    for a sequence of one CTA and for one that is joined."""
+    cache = Cache([9000, 20, 1], heads, dim, page, 55)
+    q = _query(3, heads * 8, dim, 56)
+    cache.v.global_scale.fill_(1.5)
+    want, want_lse = cache.attend(q.to(DEV))
+    cache.v.global_scale.fill_(0.75 * 2.0 ** exponent if exponent > 0 else 1.5 * 2.0 ** exponent)
+    o, lse = cache.attend(q.to(DEV))
+    factor = 2.0 ** (1 - exponent) if exponent > 0 else 2.0 ** -exponent
+    # BF16 rounds less than 2^-126 to coarser steps (zeros are the many codes of 0 of the sequence of one token)
+    normal = ((want.double() * factor).abs() >= 2.0 ** -126) | (want == 0)
+    assert torch.equal((want.double() * factor)[normal], o.double()[normal]) and torch.equal(lse, want_lse)
+    assert normal.double().mean() > 0.99
