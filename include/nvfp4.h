@@ -444,15 +444,14 @@ NVFP4_API nvfp4_status nvfp4_kv_read(const nvfp4_tensor *K, const nvfp4_tensor *
  * page_size:
  *   s_t = scale * q_h . k_t,  o_h = sum_t exp(s_t) v_t / sum_t exp(s_t),
  *   d_lse[b * heads_q + h] = log sum_t exp(s_t)   (d_lse may be NULL)
- * with k, v the exact restored values, q to 2^-29 of a head's largest, scores
- * and sums in FP32.  The weights
- * that multiply v are rounded to FP16 (by 2^-11 of each, or 2^-31 of the
- * largest of a head for small ones; nvfp4_attention_decode multiplies them
- * unrounded), o to BF16 once.  A score past FP32's range makes its head NaN.
- * A sequence of length 0 gives o = 0 and lse = -inf.  A length past
- * table_pages * page_size (or below 0) is cut to it (to 0) and recorded as
- * NVFP4_ERR_INVALID_ARG; tokens on a page outside of the pool take no part and
- * are recorded alike.
+ * with k, v the exact restored values, q exact down to 2^-29 of a head's
+ * largest, scores and sums in FP32.  The weights that multiply v are rounded to
+ * FP16 (by 2^-11 of each, or 2^-31 of the largest of a head for small ones;
+ * nvfp4_attention_decode multiplies them unrounded), o to BF16 once.  A score
+ * past FP32's range makes its head NaN.  A sequence of length 0 gives o = 0 and
+ * lse = -inf.  A length past table_pages * page_size (or below 0) is cut to it
+ * (to 0) and recorded as NVFP4_ERR_INVALID_ARG; tokens on a page outside of the
+ * pool take no part and are recorded alike.
  * q, o  : BF16 [sequences][heads_q][head_dim], strides in elements, multiples
  *         of 8; 16-byte aligned.  o == q with equal strides works in place;
  *         they may not overlap in part.  head_dim = K->cols / heads_kv: 64,

@@ -29,7 +29,7 @@
 // scales are whole 16-byte groups, a stage's parts are boxes of a 3-D tiled
 // TMA load (bytes of a head x 16 rows x heads), swizzled by it; else each
 // token's row is looked up and copied in 16-byte pieces by cp.async to the
-// same places (64 x 8192 in pages of 20 tokens: 139 us; with addresses worked
+// same places (64 x 8192 in pages of 20 tokens: 140 us; with addresses worked
 // out piece by piece 27 % more, the copying warps' instructions being the
 // bound).  Computing warps that refilled the ring themselves took 150 us where
 // a producer warp took 130 (registers).

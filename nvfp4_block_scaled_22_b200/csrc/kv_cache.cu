@@ -15,7 +15,7 @@
 //
 // Both are bound by memory (2.56 bytes a value): 131072 rows of 2 x 1024
 // values are read back in 108 us (6.4 TB/s), 16384 tokens of 2 x 8 x 128
-// written in 17.8 us (4.8 TB/s, launch included), with rotated keys in 24.2
+// written in 17.8 us (4.8 TB/s, launch included), with rotated keys in 24.3
 // us (interleaved 27.3): the table rows are loaded behind slot and position,
 // outside of the one item that a thread fetches ahead, and 19 warps an SM do
 // not hide that (a warp waits for loads 3.7 cycles an instruction issued; 57 %

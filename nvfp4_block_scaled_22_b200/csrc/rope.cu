@@ -15,7 +15,7 @@
 // in 47.6 us, 6.4 TB/s; interleaved 46.4; 4099 x 40 x 128 interleaved, half
 // rotated, in 14.5 us).  The table, made once, is bound by its arithmetic: 125
 // instructions an entry of FP64 sine and cosine and a division (131072
-// positions x 64 pairs in 36.3 us, 80 % of the issue slots; its bytes: 10.2 us).
+// positions x 64 pairs in 36.4 us, 80 % of the issue slots; its bytes: 10.2 us).
 #include <cstdint>
 #include <cuda_runtime.h>
 
